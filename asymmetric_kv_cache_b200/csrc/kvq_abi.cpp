@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -14,7 +15,9 @@
 #include <vector>
 
 #include "kvq.h"
+#include "kvq_attend_plan.h"
 #include "kvq_internal.h"
+#include "kvq_reorder_plan.h"
 #include "kvq_split.h"
 
 struct kvq_cache {
@@ -25,6 +28,7 @@ struct kvq_cache {
   size_t buf_bytes;
   std::vector<int32_t> lens;   // host mirror of the device lengths
   int max_ctas[2];             // decode CTA caps, narrow / wide (0 until queried)
+  int attend_ctas;             // resident attend CTAs (0 until queried)
 };
 
 namespace {
@@ -202,6 +206,7 @@ kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_buf, size_t bytes, 
   c->buf_bytes = bytes;
   c->lens.assign(cfg->max_seqs, 0);
   c->max_ctas[0] = c->max_ctas[1] = 0;
+  c->attend_ctas = 0;
   *out = c;
   return ok();
 }
@@ -407,6 +412,220 @@ kvq_status kvq_decode_noalloc(kvq_cache* cache, const void* q, kvq_dtype q_dtype
                            static_cast<unsigned char*>(scratch), n_seq, cache->max_ctas, max_grid,
                            cache->buf, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+  return ok();
+}
+
+kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const int32_t* n_q,
+                      int32_t n_seq, const kvq_scores* scores, void* out, void* workspace,
+                      size_t ws_bytes, void* stream) {
+  if (!cache) return fail(KVQ_ERR_NULL, "cache is NULL");
+  if (n_seq < 0) return fail(KVQ_ERR_ARG, "n_seq %d < 0", n_seq);
+  if (n_seq > cache->cfg.max_seqs)
+    return fail(KVQ_ERR_CAPACITY, "n_seq %d > max_seqs %d", n_seq, cache->cfg.max_seqs);
+  if (n_seq > 0 && !n_q) return fail(KVQ_ERR_NULL, "n_q is NULL");
+  kvq_status s = dtype_ok(q_dtype);
+  if (s != KVQ_OK) return s;
+  const kvq::Geom& g = cache->geom;
+  kvq_scores sc = {};
+  if (scores) sc = *scores;
+  if (!std::isfinite(sc.scale) || sc.scale < 0.f || !std::isfinite(sc.cap) || sc.cap < 0.f)
+    return fail(KVQ_ERR_ARG, "scale and cap must be finite and >= 0 (got %g, %g)", sc.scale, sc.cap);
+  if (sc.window < 0) return fail(KVQ_ERR_ARG, "window %d < 0", sc.window);
+  if (!aligned(sc.slopes, 4) || !aligned(sc.prefix, 4))
+    return fail(KVQ_ERR_ALIGN, "slopes and prefix must be 4-byte aligned");
+  int64_t total = 0;
+  for (int b = 0; b < n_seq; ++b) {
+    if (n_q[b] < 0) return fail(KVQ_ERR_ARG, "n_q[%d] = %d < 0", b, n_q[b]);
+    if (n_q[b] > 0 && cache->lens[b] <= 0) return fail(KVQ_ERR_EMPTY, "sequence %d is empty", b);
+    if (n_q[b] > cache->lens[b])
+      return fail(KVQ_ERR_ARG, "n_q[%d] = %d: sequence %d holds %d tokens", b, n_q[b], b, cache->lens[b]);
+    total += n_q[b];
+  }
+  if (total == 0) return ok();
+  if (total * g.hq > INT32_MAX / 2)
+    return fail(KVQ_ERR_ARG, "more than 2^30 query rows in one call");
+  if (!q || !out || !workspace) return fail(KVQ_ERR_NULL, "q, out or workspace is NULL");
+  if (!aligned(q, 16) || !aligned(out, 16)) return fail(KVQ_ERR_ALIGN, "q and out must be 16-byte aligned");
+  if (!aligned(workspace, 256)) return fail(KVQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  if ((int64_t)ws_bytes < cache->ws.total)
+    return fail(KVQ_ERR_BUFFER_TOO_SMALL, "workspace has %zu bytes, needs %lld", ws_bytes,
+                (long long)cache->ws.total);
+  if (cache->attend_ctas == 0) {
+    cudaError_t e = kvq::attend_max_ctas(g, &cache->attend_ctas);
+    if (e != cudaSuccess) return cuda_fail(e, "attend occupancy");
+  }
+  kvq::AttendArgs a = {};
+  a.cache = cache->buf;
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.out = out;
+  a.ws = static_cast<unsigned char*>(workspace);
+  a.scale = sc.scale > 0.f ? sc.scale : 1.0f / std::sqrt((float)g.d);
+  a.cap = sc.cap;
+  a.score_window = sc.window;
+  a.slopes = sc.slopes;
+  a.prefix = sc.prefix;
+  static thread_local kvq::AttendSeqs seqs;
+  int64_t row = 0;
+  for (int s0 = 0; s0 < n_seq; s0 += kvq::kAttendMaxSeqs) {
+    const int n = std::min(kvq::kAttendMaxSeqs, n_seq - s0);
+    const bool split = kvq::plan_attend(g, cache->lens.data(), n_q, s0, n, sc.window,
+                                        cache->attend_ctas, &row, &seqs);
+    if (seqs.piece_off[n] == 0) continue;
+    cudaError_t e = kvq::launch_attend(g, cache->ws, a, seqs, split, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "attend launch");
+  }
+  return ok();
+}
+
+namespace {
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+}  // namespace
+
+kvq_status kvq_norm_rotary(kvq_cache* cache, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, kvq_dtype dtype,
+                           const int32_t* n_new, int32_t n_seq, const kvq_rotary* rot, void* q_out,
+                           void* k_out, void* v_out, kvq_dtype out_dtype, void* stream) {
+  if (!cache || !rot) return fail(KVQ_ERR_NULL, "cache or rotary parameters are NULL");
+  if (n_seq < 0) return fail(KVQ_ERR_ARG, "n_seq %d < 0", n_seq);
+  if (n_seq > cache->cfg.max_seqs)
+    return fail(KVQ_ERR_CAPACITY, "n_seq %d > max_seqs %d", n_seq, cache->cfg.max_seqs);
+  if (n_seq > 0 && !n_new) return fail(KVQ_ERR_NULL, "n_new is NULL");
+  kvq_status s = dtype_ok(dtype);
+  if (s == KVQ_OK) s = dtype_ok(out_dtype);
+  if (s != KVQ_OK) return s;
+  const kvq::Geom& g = cache->geom;
+  if (rot->n_pairs < 1 || rot->n_pairs > g.d / 2)
+    return fail(KVQ_ERR_ARG, "n_pairs %d outside [1, head_dim / 2 = %d]", rot->n_pairs, g.d / 2);
+  if (rot->interleaved != 0 && rot->interleaved != 1)
+    return fail(KVQ_ERR_ARG, "interleaved must be 0 or 1 (got %d)", rot->interleaved);
+  if (!std::isfinite(rot->eps) || rot->eps < 0.f)
+    return fail(KVQ_ERR_ARG, "eps must be finite and >= 0 (got %g)", rot->eps);
+  if (rot->positions) {
+    if (rot->n_axes < 1 || rot->n_axes > 4)
+      return fail(KVQ_ERR_ARG, "n_axes %d outside [1, 4]", rot->n_axes);
+    int64_t sum = 0;
+    for (int i = 0; i < rot->n_axes; ++i) {
+      if (rot->sections[i] < 0) return fail(KVQ_ERR_ARG, "sections[%d] < 0", i);
+      sum += rot->sections[i];
+    }
+    if (sum != rot->n_pairs)
+      return fail(KVQ_ERR_ARG, "the sections hold %lld pairs, n_pairs is %d", (long long)sum, rot->n_pairs);
+  }
+  int64_t total = 0;
+  for (int b = 0; b < n_seq; ++b) {
+    if (n_new[b] < 0) return fail(KVQ_ERR_ARG, "n_new[%d] = %d < 0", b, n_new[b]);
+    total += n_new[b];
+  }
+  if (total == 0) return ok();
+  if (total > INT32_MAX) return fail(KVQ_ERR_ARG, "more than 2^31 rows in one call");
+  if (!q || !k || !q_out || !k_out || !rot->inv_freq)
+    return fail(KVQ_ERR_NULL, "q, k, q_out, k_out or inv_freq is NULL");
+  if (!v != !v_out) return fail(KVQ_ERR_NULL, "v and v_out go together");
+  const int64_t es = dtype == KVQ_FP32 ? 4 : 2, os = out_dtype == KVQ_FP32 ? 4 : 2;
+  const int64_t qw = (int64_t)g.hq * g.d, kw = (int64_t)g.hkv * g.d;
+  if (q_stride < qw || k_stride < kw || (v && v_stride < kw))
+    return fail(KVQ_ERR_ARG, "a row stride is smaller than its row");
+  if (q_stride > INT32_MAX || k_stride > INT32_MAX || (v && v_stride > INT32_MAX))
+    return fail(KVQ_ERR_ARG, "a row stride of more than 2^31 elements");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16) || q_stride * es % 16 || k_stride * es % 16 ||
+      (v && v_stride * es % 16))
+    return fail(KVQ_ERR_ALIGN, "rows of q, k, v and the outputs must be 16-byte aligned");
+  if (!aligned(rot->q_weight, 16) || !aligned(rot->k_weight, 16) || !aligned(rot->inv_freq, 4) ||
+      !aligned(rot->positions, 4))
+    return fail(KVQ_ERR_ALIGN, "weights must be 16-byte aligned, inv_freq and positions 4-byte");
+  {
+    const void* in[3] = {q, k, v};
+    const int64_t in_n[3] = {((total - 1) * q_stride + qw) * es, ((total - 1) * k_stride + kw) * es,
+                             ((total - 1) * v_stride + kw) * es};
+    const void* o[3] = {q_out, k_out, v_out};
+    const int64_t o_n[3] = {total * qw * os, total * kw * os, total * kw * os};
+    for (int i = 0; i < 3; ++i)
+      for (int j = 0; j < 3; ++j)
+        if (overlap(o[i], o_n[i], in[j], in_n[j]) || (i != j && overlap(o[i], o_n[i], o[j], o_n[j])))
+          return fail(KVQ_ERR_ARG, "an output overlaps an input or another output");
+  }
+  kvq::RotaryArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.q_weight = rot->q_weight;
+  a.k_weight = rot->k_weight;
+  a.eps = rot->eps;
+  a.inv_freq = rot->inv_freq;
+  a.n_pairs = rot->n_pairs;
+  a.interleaved = rot->interleaved;
+  a.positions = rot->positions;
+  a.n_axes = rot->positions ? rot->n_axes : 0;
+  for (int i = 0; i < a.n_axes; ++i) a.sections[i] = rot->sections[i];
+  a.lens = reinterpret_cast<const int32_t*>(cache->buf + g.lens_off);
+  a.rows = total;
+  a.hq = g.hq;
+  a.hkv = g.hkv;
+  static thread_local kvq::RotarySeqs seqs;
+  int64_t row = 0;
+  for (int s0 = 0; s0 < n_seq; s0 += kvq::kAttendMaxSeqs) {
+    const int n = std::min(kvq::kAttendMaxSeqs, n_seq - s0);
+    seqs.n = n;
+    seqs.seq0 = s0;
+    seqs.row0 = row;
+    int64_t rows = 0;
+    for (int i = 0; i < n; ++i) {
+      seqs.row_off[i] = (int32_t)rows;
+      rows += n_new[s0 + i];
+    }
+    row += rows;
+    if (rows == 0) continue;
+    cudaError_t e = kvq::launch_norm_rotary(g.d, dtype, out_dtype, a, seqs, (int)rows, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "norm_rotary launch");
+  }
+  return ok();
+}
+
+kvq_status kvq_reorder(kvq_cache* cache, const int32_t* parent, int32_t n_seq,
+                       int32_t shared_tokens, void* stream) {
+  if (!cache) return fail(KVQ_ERR_NULL, "cache is NULL");
+  if (n_seq < 0) return fail(KVQ_ERR_ARG, "n_seq %d < 0", n_seq);
+  if (n_seq > cache->cfg.max_seqs)
+    return fail(KVQ_ERR_CAPACITY, "n_seq %d > max_seqs %d", n_seq, cache->cfg.max_seqs);
+  if (n_seq > 0 && !parent) return fail(KVQ_ERR_NULL, "parent is NULL");
+  if (shared_tokens < 0) return fail(KVQ_ERR_ARG, "shared_tokens %d < 0", shared_tokens);
+  const kvq::Geom& g = cache->geom;
+  for (int b = 0; b < n_seq; ++b) {
+    if (parent[b] < 0 || parent[b] >= cache->cfg.max_seqs)
+      return fail(KVQ_ERR_ARG, "parent[%d] = %d outside [0, max_seqs = %d)", b, parent[b],
+                  cache->cfg.max_seqs);
+    if (parent[b] != b && shared_tokens > std::min(cache->lens[b], cache->lens[parent[b]]))
+      return fail(KVQ_ERR_ARG, "sequences %d and %d cannot share %d tokens (they hold %d and %d)", b,
+                  parent[b], shared_tokens, cache->lens[b], cache->lens[parent[b]]);
+  }
+  const std::vector<kvq::ReorderMove> all = kvq::plan_reorder(parent, n_seq, cache->cfg.max_seqs);
+  static thread_local kvq::ReorderMoves mv;
+  for (size_t at = 0; at < all.size();) {
+    const size_t from = at;
+    at = kvq::next_reorder_launch(all, at, &mv);
+    int64_t bytes = 0;                       // of the longest move of the launch, per kv head
+    for (size_t i = from; i < at; ++i) {
+      const int n = cache->lens[all[i].src];
+      bytes = std::max(bytes, (int64_t)kvq::quantized_groups_s(n, g.G, g.window, g.sink) * g.block_bytes);
+    }
+    const int64_t tiles = ((bytes >> 15) + 2 + (g.sink ? 1 : 0) + (g.tail_bytes >> 15)) * g.hkv;
+    cudaError_t e = kvq::launch_reorder(g, cache->buf, mv, shared_tokens, tiles, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "reorder launch");
+  }
+  std::vector<int32_t> old(cache->lens);
+  for (int b = 0; b < n_seq; ++b) cache->lens[b] = old[parent[b]];
   return ok();
 }
 

@@ -1,0 +1,564 @@
+// Attention of one or more new tokens per sequence over the quantized cache
+// (kvq_attend), on register tiles.
+//
+//   out_r = sum_j softmax_j(s_rj) v_j,   s_rj = cap(scale q_r . k_j) - slope_h |p_r - j|
+//
+// over the visible keys of row r = (token at position p_r, query head h):
+// (j <= p_r and p_r - j < window) or j < prefix.
+//
+// Unit: (sequence, kv head, tile of 8 rows of the kv head's n_q * gqa rows,
+// token-major, so a tile's rows are neighbours in time).  A unit's visible
+// key blocks and 16-token pieces of the fp16 sink and tail form a list, cut
+// into equal pieces (one CTA of 4 warps each) when there are fewer units
+// than CTAs on the chip; the warps of a CTA take every fourth entry, each
+// with its own bulk-copied ring and its own running maximum and sum.
+//
+// One block (32 or 64 tokens, taken 32 at a time) is, per warp:
+//   * k = s_c code + z_c, so q.k = sum_c (q_c s_c) code_c + sum_c q_c z_c.
+//     The codes go to the tensor core as exact small integers; q_c s_c is an
+//     fp16 value plus its exact residual (one fused multiply-subtract), rows
+//     0-7 of the 16-row A operand holding the one and rows 8-15 the other,
+//     so the logits carry ~22 bits at no extra tile.
+//   * p goes to fp16 (one rounding, relative 2^-11 at most), v = s code + z
+//     to fp16 (one fused rounding).  With at most 4 rows, columns 4-7 of the
+//     value product are free and carry p's residual: p is then exact to 2^-22.
+//   * all sums, maxima and the two accumulators are fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kvq_device.cuh"
+#include "kvq_internal.h"
+
+namespace kvq {
+
+constexpr int kAttWarps = 4;
+constexpr int kAttThreads = kAttWarps * 32;
+constexpr int kAttStages = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D, int KB, int VB, int G>
+struct AttCfg {
+  static constexpr int KT = D / 16, MT = D / 16, J = D / G;
+  static constexpr int V_BYTES = G * D * VB / 8 + 4 * G * J;   // value sections
+  template <int KBL>
+  static constexpr int k_bytes() { return G * D * KBL / 8 + 4 * D; }
+  static constexpr int BLK = k_bytes<KB>() + V_BYTES;
+  static constexpr int QF = 0;                                  // query fragments
+  static constexpr int RING = KT * 32 * 16;
+  static constexpr int RING_BYTES = kAttWarps * kAttStages * BLK;
+  // merge area (over the ring): per warp [8][D + 2] floats
+  static constexpr int MERGE_BYTES = kAttWarps * kAttendRows * (D + 2) * 4;
+  static constexpr int BAR = RING + (RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES);
+  static constexpr int SMEM = BAR + kAttWarps * kAttStages * 8;
+  static_assert(BLK % 16 == 0 && RING % 16 == 0 && BAR % 8 == 0, "aligned areas");
+};
+
+// What a row's scores need (row g8 of the tile, the same in its four lanes).
+struct RowRule {
+  int pos, prefix, window;   // window: INT_MAX when there is none
+  float scale2, cap2, inv_cap2, slope2;   // times log2(e) where they end in an exponent
+};
+
+// The score of key j in the exp2 domain.  tanh(x) = 1 - 2 / (1 + e^(2x)): its
+// error of a few 2^-24 is absolute, and the cap multiplies it, 3e-6 at 50.
+__device__ __forceinline__ float att_score(const RowRule& rr, float dot, int j) {
+  float s;
+  if (rr.cap2 != 0.f) {
+    const float e = fast_exp2(dot * rr.inv_cap2);
+    s = rr.cap2 - __fdividef(2.f * rr.cap2, 1.f + e);
+    s = e > 1e37f ? rr.cap2 : s;
+  } else {
+    s = dot * rr.scale2;
+  }
+  const int far = rr.pos - j;
+  return s - rr.slope2 * (float)(far < 0 ? -far : far);
+}
+__device__ __forceinline__ bool att_visible(const RowRule& rr, int j) {
+  return (j <= rr.pos && rr.pos - j < rr.window) || j < rr.prefix;
+}
+
+template <int MT>
+struct AttState {
+  float o[MT][4];   // O^T: channels 16 mt + g8 (+ 8), rows 2 i4, 2 i4 + 1
+  float m, l;       // row g8: running maximum (exp2 domain), sum over this lane's keys
+};
+
+// Folds 8 NT keys' scores into the running softmax and returns the weights
+// as the B operand of the value product.
+template <int NT, int MT>
+__device__ __forceinline__ void att_softmax(AttState<MT>& st, float (&s)[NT][2],
+                                            uint32_t (&pb)[NT], bool dup, int lane) {
+  const int i4 = lane & 3;
+  float mx = s[0][0];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][0], s[nt][1]));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  const float mn = fmaxf(st.m, mx);
+  const float base = mn == -INFINITY ? 0.f : mn;   // no key seen yet: every weight is 0
+  const float alpha = fast_exp2(st.m - base);
+  st.m = mn;
+  if (__any_sync(0xffffffffu, alpha != 1.f)) {
+    st.l *= alpha;
+    const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * i4);
+    const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * i4 + 4);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      st.o[mt][0] *= a0;
+      st.o[mt][1] *= a1;
+      st.o[mt][2] *= a0;
+      st.o[mt][3] *= a1;
+    }
+  }
+  const bool low = dup && lane >= 16;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float p0 = fast_exp2(s[nt][0] - base), p1 = fast_exp2(s[nt][1] - base);
+    st.l += p0 + p1;
+    uint32_t h = pack_h2(p0, p1);
+    if (low) {
+      const float2 f = __half22float2(u32_as_h2(h));
+      h = pack_h2(p0 - f.x, p1 - f.y);
+    }
+    pb[nt] = h;
+  }
+}
+
+// Turns the two halves of the 16-row product (value and residual parts of
+// the query) into the scores of row g8.
+template <int NT>
+__device__ __forceinline__ void att_scores(const RowRule& rr, const float (&c)[NT][4], float bias,
+                                           int pos0, bool masked, int lane, float (&s)[NT][2]) {
+  const int i4 = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = pos0 + 8 * nt + 2 * i4 + e;
+      const float x = att_score(rr, c[nt][e] + c[nt][e + 2] + bias, j);
+      s[nt][e] = !masked || att_visible(rr, j) ? x : -INFINITY;
+    }
+  }
+}
+
+// 32 tokens (half hf of a 64-token block) of a block in shared memory, with
+// KBL-bit keys.
+template <int D, int KBL, int VB, int G>
+__device__ __forceinline__ void att_block(AttState<D / 16>& st, const RowRule& rr,
+                                          const unsigned char* blk, const uint4* qf, int hf,
+                                          int pos0, bool masked, bool dup, int lane) {
+  constexpr int KT = D / 16, MT = D / 16, J = D / G, NT = 4;
+  constexpr int LBK = D * KBL / 32, WK = LBK / 4, FK = 16 / KBL;
+  constexpr int WV = D * VB / 64, FV = 16 / VB;
+  constexpr int OFF_S = G * D * KBL / 8, OFF_Z = OFF_S + 2 * D, OFF_V = OFF_Z + 2 * D,
+                OFF_VS = OFF_V + G * D * VB / 8, OFF_VZ = OFF_VS + 2 * G * J;
+  const int i4 = lane & 3;
+  float c[NT][4], zc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+  uint32_t kw[NT][WK];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+    lds_words<WK>(reinterpret_cast<const uint32_t*>(blk + (4 * hf + nt) * 32 * LBK + lane * LBK), kw[nt]);
+  const uint32_t* ks = reinterpret_cast<const uint32_t*>(blk + OFF_S) + i4 * (D / 8);
+  const uint32_t* kz = reinterpret_cast<const uint32_t*>(blk + OFF_Z) + i4 * (D / 8);
+  static_for<KT / 2>([&](auto kc) {
+    constexpr int k2 = decltype(kc)::value;
+    uint32_t s4[4], z4[4];
+    lds_words<4>(ks + 4 * k2, s4);
+    lds_words<4>(kz + 4 * k2, z4);
+    static_for<2>([&](auto hc) {
+      constexpr int kt = 2 * k2 + decltype(hc)::value;
+      constexpr int w0 = 2 * decltype(hc)::value;
+      const uint4 q = qf[kt * 32 + lane];      // {value, residual} of channels +0,1 and +8,9
+      uint32_t a[4];
+      a[0] = hmul2_b(q.x, s4[w0]);
+      a[2] = hmul2_b(q.z, s4[w0 + 1]);
+      a[1] = hfma2_b(q.y, s4[w0], hfma2_negc_b(q.x, s4[w0], a[0]));
+      a[3] = hfma2_b(q.w, s4[w0 + 1], hfma2_negc_b(q.z, s4[w0 + 1], a[2]));
+      mma16816(zc, q.x, q.y, q.z, q.w, z4[w0], z4[w0 + 1]);
+      static_for<NT>([&](auto nc) {
+        constexpr int nt = decltype(nc)::value;
+        constexpr int p0 = 2 * kt, p1 = 2 * kt + 1;
+        const uint32_t b0 = unpack_pair<KBL, p0 % FK>(kw[nt][p0 / FK]);
+        const uint32_t b1 = unpack_pair<KBL, p1 % FK>(kw[nt][p1 / FK]);
+        mma16816(c[nt], a[0], a[1], a[2], a[3], b0, b1);
+      });
+    });
+  });
+  float s[NT][2];
+  uint32_t pb[NT];
+  att_scores<NT>(rr, c, zc[0] + zc[2], pos0, masked, lane, s);
+  att_softmax<NT, MT>(st, s, pb, dup, lane);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int kv = 2 * hf + t;
+    uint32_t vw[WV];
+    lds_words<WV>(reinterpret_cast<const uint32_t*>(blk + OFF_V) + (kv * 32 + lane) * WV, vw);
+    uint32_t vs[2 * J], vz[2 * J];
+    lds_words<2 * J>(reinterpret_cast<const uint32_t*>(blk + OFF_VS) + (4 * kv + i4) * J * 2, vs);
+    lds_words<2 * J>(reinterpret_cast<const uint32_t*>(blk + OFF_VZ) + (4 * kv + i4) * J * 2, vz);
+    static_for<MT>([&](auto mc) {
+      constexpr int mt = decltype(mc)::value;
+      constexpr int j = 16 * mt / G, w = mt / (FV / 4), u = mt % (FV / 4);
+      const uint32_t a0 = hfma2_b(unpack_pair<VB, 2 * u>(vw[w]), vs[2 * j], vz[2 * j]);
+      const uint32_t a1 = hfma2_b(unpack_pair<VB, 2 * u + 1>(vw[w]), vs[2 * j], vz[2 * j]);
+      const uint32_t a2 = hfma2_b(unpack_pair<VB, 2 * u + FV / 2>(vw[w]), vs[2 * j + 1], vz[2 * j + 1]);
+      const uint32_t a3 = hfma2_b(unpack_pair<VB, 2 * u + 1 + FV / 2>(vw[w]), vs[2 * j + 1], vz[2 * j + 1]);
+      mma16816(st.o[mt], a0, a1, a2, a3, pb[2 * t], pb[2 * t + 1]);
+    });
+  }
+}
+
+// 16 fp16 tokens: K rows token-major at k, V token pairs [8][D][2] at v
+// (global memory); `valid` of them hold tokens (the rest may hold anything).
+template <int D>
+__device__ __forceinline__ void att_fp16(AttState<D / 16>& st, const RowRule& rr, const __half* k,
+                                         const __half* v, const uint4* qf, int pos0, int valid,
+                                         bool dup, int lane) {
+  constexpr int KT = D / 16, MT = D / 16, NT = 2;
+  const int g8 = lane >> 2, i4 = lane & 3;
+  float c[NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    const uint4 q = qf[kt * 32 + lane];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t* row = reinterpret_cast<const uint32_t*>(k + (8 * nt + g8) * D + 16 * kt) + i4;
+      mma16816(c[nt], q.x, q.y, q.z, q.w, row[0], row[4]);
+    }
+  }
+  float s[NT][2];
+  uint32_t pb[NT];
+  att_scores<NT>(rr, c, 0.f, pos0, true, lane, s);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (8 * nt + 2 * i4 + e >= valid) s[nt][e] = -INFINITY;
+  att_softmax<NT, MT>(st, s, pb, dup, lane);
+  // tokens past `valid` have weight 0, and their values (which may be NaN)
+  // are replaced by 0
+  auto keep = [&](int t) {
+    return (t < valid ? 0x0000FFFFu : 0u) | (t + 1 < valid ? 0xFFFF0000u : 0u);
+  };
+  const uint32_t m0 = keep(2 * i4), m1 = keep(2 * i4 + 8);
+  const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const uint32_t a0 = vw[i4 * D + 16 * mt + g8] & m0, a1 = vw[i4 * D + 16 * mt + g8 + 8] & m0;
+    const uint32_t a2 = vw[(i4 + 4) * D + 16 * mt + g8] & m1,
+                   a3 = vw[(i4 + 4) * D + 16 * mt + g8 + 8] & m1;
+    mma16816(st.o[mt], a0, a1, a2, a3, pb[0], pb[1]);
+  }
+}
+
+// Stores row r (of the kv head's rows) from a warp that holds the weighted sum
+// y (D / 32 channels a lane) and the weights' sum l: rotated back where the
+// cache is rotated; a row that sees no key is 0.
+template <int D>
+__device__ __forceinline__ void attend_store_row(const Geom& g, const AttendArgs& a,
+                                                 const AttendSeqs& seqs, int sq, int h, int r,
+                                                 float (&y)[D / 32], float l, int lane) {
+  constexpr int V = D / 32;
+  const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+#pragma unroll
+  for (int i = 0; i < V; ++i) y[i] = l > 0.f || l != l ? y[i] * inv : 0.f;
+  if (g.rotate) {
+    fwht_lanes<D, V>(y, lane);
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] *= rot_scale<D>();
+  }
+  __half* out = reinterpret_cast<__half*>(a.out) +
+                ((int64_t)(seqs.row_off[sq] + r / g.gqa) * g.hq + h * g.gqa + r % g.gqa) * D + lane * V;
+#pragma unroll
+  for (int i = 0; i < V; i += 2)
+    *reinterpret_cast<uint32_t*>(out + i) = pack_h2(y[i], y[i + 1]);
+}
+
+template <int D, int KB, int VB, int G>
+__global__ void __launch_bounds__(kAttThreads, 4)
+    attend_kernel(const Geom g, const WsLayout w, const AttendArgs a, const AttendSeqs seqs) {
+  using C = AttCfg<D, KB, VB, G>;
+  extern __shared__ __align__(128) unsigned char att_smem[];
+  uint4* qf = reinterpret_cast<uint4*>(att_smem + C::QF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(att_smem + C::BAR);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2;
+  int32_t* err = reinterpret_cast<int32_t*>(a.ws + w.err_off);
+
+  // ---- this piece: sequence, kv head, row tile, part of the key list
+  int sq;
+  {
+    int lo = 0, hi = seqs.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (seqs.piece_off[mid] <= (int)blockIdx.x) lo = mid; else hi = mid;
+    }
+    sq = lo;
+  }
+  const int nq = seqs.n_q[sq], R = nq * g.gqa;
+  const int tiles = (R + kAttendRows - 1) / kAttendRows;
+  const int local = blockIdx.x - seqs.piece_off[sq];
+  const int parts = (seqs.piece_off[sq + 1] - seqs.piece_off[sq]) / (g.hkv * tiles);
+  const int part = local % parts, h = local / parts / tiles, tile = local / parts % tiles;
+  const int r0 = tile * kAttendRows, nr = min(kAttendRows, R - r0);
+  const bool dup = nr <= 4;
+  const int seq = seqs.seq0 + sq;
+  const int n = min(max(reinterpret_cast<const int32_t*>(a.cache + g.lens_off)[seq], 0), g.max_tokens);
+
+  if (lane == 0) {
+    for (int s = 0; s < kAttStages; ++s) mbar_init(&bars[warp * kAttStages + s], 1);
+    fence_mbar_init();
+  }
+
+  // ---- the visible keys: blocks [0, gA) and [gB, gC), the sink, the tail
+  const int S = min(n, g.sink), ng = quantized_groups_s(n, G, g.window, g.sink);
+  const int N = S + ng * G, T = n - N;                  // first tail position, tail tokens
+  const int window = a.score_window > 0 ? a.score_window : 0x7fffffff;
+  const int prefix = a.prefix ? min(max(a.prefix[seq], 0), n) : 0;
+  const int p_lo = n - nq + r0 / g.gqa, p_hi = n - nq + (r0 + nr - 1) / g.gqa;
+  const int first = max(0, p_lo >= window ? p_lo - window + 1 : 0);
+  const int gA0 = min(ng, max(0, (prefix - S + G - 1) / G));
+  const int gB = min(ng, max(0, first - S) / G);
+  const int gC = max(gA0, min(ng, max(0, (p_hi + 1 - S + G - 1) / G)));
+  const int gA = min(gA0, gB);
+  const int nblk = gA + max(0, gC - gB), nsink = (S + 15) / 16, ntail = (T + 15) / 16;
+  const int total = nblk + nsink + ntail;
+  const int it0 = (int)((int64_t)total * part / parts), it1 = (int)((int64_t)total * (part + 1) / parts);
+
+  const unsigned char* blocks =
+      a.cache + g.blocks_off + ((int64_t)seq * g.hkv + h) * g.max_groups * g.block_bytes;
+  unsigned char* ring = att_smem + C::RING + warp * kAttStages * C::BLK;
+  auto group_of = [&](int it) { return it < gA ? it : gB + it - gA; };
+  auto two_bit = [&](int grp) {
+    return KB == 4 && g.akvq_delta && akvq_key_bits(grp, n, G, g.akvq_delta) == 2;
+  };
+  auto fetch = [&](int it, int s) {     // one lane
+    const int grp = group_of(it);
+    const uint32_t bytes = two_bit(grp) ? (uint32_t)g.a2_bytes : (uint32_t)C::BLK;
+    mbar_arrive_expect_tx(&bars[warp * kAttStages + s], bytes);
+    bulk_copy_g2s(ring + s * C::BLK, blocks + (int64_t)grp * g.block_bytes, bytes,
+                  &bars[warp * kAttStages + s]);
+  };
+  __syncwarp();
+  const int b1 = min(it1, nblk);        // this piece's blocks: [it0, b1), warp + 4 i
+  if (lane == 0) {
+    for (int s = 0; s < kAttStages; ++s)
+      if (it0 + warp + kAttWarps * s < b1) fetch(it0 + warp + kAttWarps * s, s);
+  }
+
+  // ---- query rows: rotated where the cache is, value and residual parts in
+  // fragment order.  Warp w takes rows 2w and 2w + 1; row r >= nr is zero,
+  // but with at most 4 rows the upper 4 repeat the lower ones.
+  {
+    constexpr int V = D / 32;
+    for (int x = 0; x < kAttendRows / kAttWarps; ++x) {
+      const int r = warp * (kAttendRows / kAttWarps) + x, rs = dup ? r & 3 : r;
+      float y[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[i] = 0.f;
+      if (rs < nr) {
+        const int qi = (r0 + rs) / g.gqa, hh = (r0 + rs) % g.gqa;
+        const int64_t at = ((int64_t)(seqs.row_off[sq] + qi) * g.hq + h * g.gqa + hh) * D + lane * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = load_as_float(a.q, at + i, a.q_dtype);
+      }
+      if (g.rotate) {
+        fwht_lanes<D, V>(y, lane);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] *= rot_scale<D>();
+      }
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const uint32_t hi = pack_h2(y[i], y[i + 1]);
+        const float2 f = __half22float2(u32_as_h2(hi));
+        const uint32_t lo = pack_h2(y[i] - f.x, y[i + 1] - f.y);
+        const int c = lane * V + i;     // channel pair: k-step c / 16, half (c % 16) / 8, quad lane
+        uint32_t* dst = reinterpret_cast<uint32_t*>(qf + (c / 16) * 32 + 4 * r + (c % 8) / 2) + (c % 16) / 8 * 2;
+        dst[0] = hi;
+        dst[1] = lo;
+      }
+    }
+  }
+  __syncthreads();
+
+  RowRule rr;
+  {
+    const int r = dup ? g8 & 3 : g8;
+    const int rc = min(r, nr - 1);
+    rr.pos = n - nq + (r0 + rc) / g.gqa;
+    rr.prefix = prefix;
+    rr.window = window;
+    rr.scale2 = a.scale * kLog2e;
+    rr.cap2 = a.cap * kLog2e;
+    rr.inv_cap2 = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+    rr.slope2 = a.slopes ? a.slopes[h * g.gqa + (r0 + rc) % g.gqa] * kLog2e : 0.f;
+  }
+  AttState<C::MT> st;
+#pragma unroll
+  for (int mt = 0; mt < C::MT; ++mt) st.o[mt][0] = st.o[mt][1] = st.o[mt][2] = st.o[mt][3] = 0.f;
+  st.m = -INFINITY;
+  st.l = 0.f;
+  // keys [pos, pos + len): seen by some row / by every row of the tile
+  auto some = [&](int pos, int len) {
+    return pos < prefix || (pos <= p_hi && pos + len > first);
+  };
+  auto every = [&](int pos, int len) {
+    return pos + len <= prefix || (pos + len - 1 <= p_lo && p_hi - pos < window);
+  };
+
+  bool ok = true;
+  int stage = 0, phase = 0;
+  for (int it = it0 + warp; it < b1; it += kAttWarps) {
+    if (ok && !mbar_wait_bounded(&bars[warp * kAttStages + stage], phase)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const int grp = group_of(it);
+    const unsigned char* blk = ring + stage * C::BLK;
+    const bool narrow = two_bit(grp);
+#pragma unroll 1
+    for (int hf = 0; hf < G / 32; ++hf) {
+      const int pos = S + grp * G + 32 * hf;
+      if (!some(pos, 32)) continue;
+      const bool masked = !every(pos, 32);
+      if constexpr (KB == 4) {
+        if (narrow) {
+          att_block<D, 2, VB, G>(st, rr, blk, qf, hf, pos, masked, dup, lane);
+          continue;
+        }
+      }
+      att_block<D, KB, VB, G>(st, rr, blk, qf, hf, pos, masked, dup, lane);
+    }
+    __syncwarp();
+    const int next = it + kAttWarps * kAttStages;
+    if (lane == 0 && next < b1) {
+      fence_proxy_async_smem();
+      fetch(next, stage);
+    }
+    if (++stage == kAttStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (!ok) {
+    // a wait ran out: record it and let the copies in flight land before the
+    // shared memory goes away
+    if (lane == 0) atomicExch(err, KVQ_ERR_DEVICE);
+    for (int s = 0; s < kAttStages; ++s)
+      mbar_wait_bounded(&bars[warp * kAttStages + s], s >= stage ? phase : phase ^ 1);
+  }
+  // ---- fp16 tokens: the sink's pieces, then the tail's
+  const __half* sink = reinterpret_cast<const __half*>(a.cache + g.sinks_off + ((int64_t)seq * g.hkv + h) * g.sink_bytes);
+  const __half* tail = reinterpret_cast<const __half*>(a.cache + g.tails_off + ((int64_t)seq * g.hkv + h) * g.tail_bytes);
+  for (int it = it0 + ((max(it0, nblk) - it0 + kAttWarps - 1 - warp) / kAttWarps) * kAttWarps + warp; it < it1;
+       it += kAttWarps) {
+    const int x = it - nblk;
+    if (x < nsink) {
+      const int t = 16 * x;
+      if (!some(t, min(16, S - t))) continue;
+      att_fp16<D>(st, rr, sink + t * D, sink + (g.sink_slots + t) * D, qf, t, S - t, dup, lane);
+    } else {
+      const int t = 16 * (x - nsink), pos = N + t;
+      if (!some(pos, min(16, T - t))) continue;
+      const int slot = (pos - S) % g.tail_slots;
+      att_fp16<D>(st, rr, tail + slot * D, tail + (g.tail_slots + slot) * D, qf, pos, T - t, dup, lane);
+    }
+  }
+
+  // ---- merge the warps (over the ring: every copy has landed)
+  st.l += __shfl_xor_sync(0xffffffffu, st.l, 1);
+  st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
+  __syncthreads();
+  float* mg = reinterpret_cast<float*>(att_smem + C::RING);
+  {
+    const int i4 = lane & 3;
+    float* mine = mg + warp * kAttendRows * (D + 2);
+#pragma unroll
+    for (int mt = 0; mt < C::MT; ++mt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mine[(2 * i4 + e) * (D + 2) + 16 * mt + g8] = st.o[mt][e];
+        mine[(2 * i4 + e) * (D + 2) + 16 * mt + g8 + 8] = st.o[mt][e + 2];
+      }
+    }
+    if (i4 == 0) {
+      mine[g8 * (D + 2) + D] = st.m;
+      mine[g8 * (D + 2) + D + 1] = st.l;
+    }
+  }
+  __syncthreads();
+  constexpr int V = D / 32;
+  for (int r = warp; r < nr; r += kAttWarps) {
+    float m = -INFINITY, l = 0.f, y[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = 0.f;
+#pragma unroll
+    for (int ww = 0; ww < kAttWarps; ++ww) m = fmaxf(m, mg[(ww * kAttendRows + r) * (D + 2) + D]);
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int ww = 0; ww < kAttWarps; ++ww) {
+      const float* row = mg + (ww * kAttendRows + r) * (D + 2);
+      const float f = fast_exp2(row[D] - base);
+      l += f * row[D + 1];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = lane * V + i;
+        y[i] += f * (dup ? row[c] + row[4 * (D + 2) + c] : row[c]);
+      }
+    }
+    if (parts > 1) {
+      float* ps = reinterpret_cast<float*>(a.ws + w.partials_off) +
+                  ((int64_t)blockIdx.x * kAttendRows + r) * (D + 4);
+#pragma unroll
+      for (int i = 0; i < V; ++i) ps[lane * V + i] = y[i];
+      if (lane == 0) {
+        ps[D] = m;
+        ps[D + 1] = l;
+      }
+    } else {
+      attend_store_row<D>(g, a, seqs, sq, h, r0 + r, y, l, lane);
+    }
+  }
+}
+
+// The kernel's shared memory is above the default limit for some blocks; the
+// attribute belongs to the device, and setting it again is harmless.
+template <int D, int KB, int VB, int G>
+cudaError_t attend_configure() {
+  return cudaFuncSetAttribute(attend_kernel<D, KB, VB, G>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, AttCfg<D, KB, VB, G>::SMEM);
+}
+template <int D, int KB, int VB, int G>
+cudaError_t attend_occupancy(int* out) {
+  int dev = 0, sms = 0, per = 0;
+  cudaError_t e = attend_configure<D, KB, VB, G>();
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attend_kernel<D, KB, VB, G>, kAttThreads,
+                                                      AttCfg<D, KB, VB, G>::SMEM);
+  *out = sms * (per > 0 ? per : 1);
+  return e;
+}
+
+#define KVQ_ATTEND_DEFINE(D_, KB_, VB_, G_)                                                       \
+  cudaError_t attend_max_ctas_##D_##_##KB_##_##VB_##_##G_(int* out) {                             \
+    return attend_occupancy<D_, KB_, VB_, G_>(out);                                               \
+  }                                                                                               \
+  cudaError_t launch_attend_##D_##_##KB_##_##VB_##_##G_(const Geom& g, const WsLayout& w,         \
+                                                        const AttendArgs& a, const AttendSeqs& s, \
+                                                        cudaStream_t stream) {                    \
+    using C = AttCfg<D_, KB_, VB_, G_>;                                                           \
+    if (g.block_bytes != C::BLK) return cudaErrorInvalidValue;                                    \
+    cudaError_t e = attend_configure<D_, KB_, VB_, G_>();                                         \
+    if (e != cudaSuccess) return e;                                                               \
+    attend_kernel<D_, KB_, VB_, G_>                                                               \
+        <<<(unsigned)s.piece_off[s.n], kAttThreads, C::SMEM, stream>>>(g, w, a, s);               \
+    return cudaGetLastError();                                                                    \
+  }
+
+}  // namespace kvq

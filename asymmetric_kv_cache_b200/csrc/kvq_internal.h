@@ -227,4 +227,75 @@ cudaError_t launch_decode_fp16(const Geom& g, const WsLayout& w, const DecodeArg
 constexpr int64_t kNoAllocScratchBytes = 8LL << 20;
 cudaError_t noalloc_scratch(void** ptr);
 
+// ---- attention of several new tokens per sequence ---------------------------
+// Sequences per attend / rotary launch (their arguments ride in the kernel
+// parameters).
+constexpr int kAttendMaxSeqs = 512;
+// Rows (query token, query head) of one unit: the N = 8 columns of the
+// P.V tile.
+constexpr int kAttendRows = 8;
+// Split pieces of one launch that write partials: their slots (kAttendRows
+// rows each) fill the decode workspace's partial region.
+constexpr int kAttendPieces = 2 * kMaxDecodeCtas;
+
+struct AttendArgs {
+  const unsigned char* cache;
+  const void* q;             // [rows][hq][d]
+  int32_t q_dtype;
+  void* out;                 // fp16 [rows][hq][d]
+  unsigned char* ws;
+  float scale, cap;          // cap = 0: none
+  int32_t score_window;      // 0: none
+  const float* slopes;       // [hq] or NULL
+  const int32_t* prefix;     // [n_seq] or NULL
+};
+
+// Sequence i of a launch is the cache's seq0 + i; its query rows start at
+// row_off[i] (n_q[i] of them) and its pieces at piece_off[i]: per (kv head,
+// row tile) the same number of pieces, tile after tile.
+struct AttendSeqs {
+  int32_t n, seq0;
+  int32_t row_off[kAttendMaxSeqs];
+  int32_t n_q[kAttendMaxSeqs];
+  int32_t piece_off[kAttendMaxSeqs + 1];
+};
+
+cudaError_t attend_max_ctas(const Geom& g, int* max_ctas);
+cudaError_t launch_attend(const Geom& g, const WsLayout& w, const AttendArgs& a,
+                          const AttendSeqs& s, bool split, cudaStream_t stream);
+#define KVQ_ATTEND_DECLARE(D_, KB_, VB_, G_)                                          \
+  cudaError_t attend_max_ctas_##D_##_##KB_##_##VB_##_##G_(int* out);                  \
+  cudaError_t launch_attend_##D_##_##KB_##_##VB_##_##G_(                              \
+      const Geom& g, const WsLayout& w, const AttendArgs& a, const AttendSeqs& s,     \
+      cudaStream_t stream);
+KVQ_DECODE_FOR_EACH(KVQ_ATTEND_DECLARE)
+
+// ---- norms of query and key heads with the position rotation ----------------
+struct RotaryArgs {
+  const void *q, *k, *v;     // v may be NULL
+  int64_t q_stride, k_stride, v_stride;   // elements between rows
+  void *q_out, *k_out, *v_out;
+  const void *q_weight, *k_weight;        // [d] of the input type, or NULL
+  float eps;
+  const float* inv_freq;     // [n_pairs]
+  int32_t n_pairs, interleaved;
+  const int32_t* positions;  // [n_axes][rows], or NULL: from the lengths
+  int32_t n_axes, sections[4];
+  const int32_t* lens;
+  int64_t rows;              // of the whole call
+  int32_t hq, hkv;
+};
+struct RotarySeqs {
+  int32_t n, seq0;
+  int64_t row0;              // the launch's first row
+  int32_t row_off[kAttendMaxSeqs];        // from row0
+};
+cudaError_t launch_norm_rotary(int d, int dtype, int out_dtype, const RotaryArgs& a,
+                               const RotarySeqs& seqs, int rows, cudaStream_t stream);
+
+// ---- reordering of sequences ---------------------------------------------
+struct ReorderMoves;         // kvq_reorder_plan.h
+cudaError_t launch_reorder(const Geom& g, unsigned char* cache, const ReorderMoves& mv,
+                           int shared_tokens, int64_t tiles, cudaStream_t stream);
+
 }  // namespace kvq

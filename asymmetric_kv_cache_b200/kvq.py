@@ -50,6 +50,19 @@ class KvqLayout(ctypes.Structure):
         "akvq_vcodes_offset", "akvq_vscale_offset", "akvq_vmin_offset")]
 
 
+class KvqScores(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
+class KvqRotary(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("n_pairs", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p),
+                ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
 _c_status = ctypes.c_int32
 _vp = ctypes.c_void_p
 _P = ctypes.POINTER
@@ -74,6 +87,13 @@ kvq_append = _sig("kvq_append", [_vp, _vp, _vp, ctypes.c_int32, _P(ctypes.c_int3
                                  ctypes.c_int32, _vp])
 kvq_decode = _sig("kvq_decode", [_vp, _vp, ctypes.c_int32, _vp, ctypes.c_int32, _vp,
                                  ctypes.c_size_t, _vp])
+kvq_attend = _sig("kvq_attend", [_vp, _vp, ctypes.c_int32, _P(ctypes.c_int32), ctypes.c_int32,
+                                 _P(KvqScores), _vp, _vp, ctypes.c_size_t, _vp])
+kvq_norm_rotary = _sig("kvq_norm_rotary",
+                       [_vp, _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp, ctypes.c_int64,
+                        ctypes.c_int32, _P(ctypes.c_int32), ctypes.c_int32, _P(KvqRotary), _vp, _vp,
+                        _vp, ctypes.c_int32, _vp])
+kvq_reorder = _sig("kvq_reorder", [_vp, _P(ctypes.c_int32), ctypes.c_int32, ctypes.c_int32, _vp])
 kvq_workspace_init = _sig("kvq_workspace_init", [_vp, ctypes.c_size_t, _vp])
 kvq_workspace_status = _sig("kvq_workspace_status", [_vp, _vp])
 kvq_cache_config = _sig("kvq_cache_config", [_vp, _P(KvqConfig)])
@@ -93,7 +113,8 @@ EXPORTED = ["kvq_status_string", "kvq_last_error", "kvq_layout_for", "kvq_cache_
             "kvq_cache_create", "kvq_cache_destroy", "kvq_reset", "kvq_append", "kvq_decode",
             "kvq_workspace_init", "kvq_workspace_status", "kvq_cache_config",
             "kvq_cache_layout", "kvq_get_lengths", "kvq_sync_lengths", "kvq_decode_noalloc",
-            "kvq_noalloc_scratch_bytes", "kvq_fp16_workspace_bytes", "kvq_decode_fp16"]
+            "kvq_noalloc_scratch_bytes", "kvq_fp16_workspace_bytes", "kvq_decode_fp16",
+            "kvq_attend", "kvq_norm_rotary", "kvq_reorder"]
 
 
 class KvqError(RuntimeError):
@@ -252,6 +273,124 @@ class KVQCache:
                                  _dev_ptr(out, "out"), q.shape[0], _stream(stream)),
               "kvq_decode_noalloc")
         return out
+
+    # ---- several new tokens per sequence, positions, reordering ----
+    def _on(self, t: torch.Tensor, name: str, dtype=None) -> torch.Tensor:
+        """t, if it lives on the cache's device (and has the type)."""
+        if t.device != self.buffer.device:
+            raise ValueError(f"{name} must be on {self.buffer.device}, got {t.device}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        return t
+
+    def _launch(self, stream, fn, name, *args):
+        """fn(*args, stream) on the cache's device (the caller's current one stays)."""
+        with torch.cuda.device(self.buffer.device):
+            check(fn(*args, _stream(stream)), name)
+
+    def _rows(self, t: torch.Tensor, name: str, rows: int, heads: int) -> int:
+        """Elements between the rows of t [rows, heads, d], each row's heads side by side."""
+        d = self.spec.head_dim
+        if tuple(t.shape) != (rows, heads, d):
+            raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(t.shape)}")
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+            raise ValueError(f"{name}: a row's heads must lie side by side")
+        return t.stride(0) if rows > 1 else heads * d
+
+    def attend(self, q: torch.Tensor, n_q, scale: float = 0.0, cap: float = 0.0, window: int = 0,
+               slopes: torch.Tensor | None = None, prefix: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of the newest ``n_q[b]`` tokens of each sequence (kvq_attend).
+
+        q: [sum(n_q), n_q_heads, d]; scale (0: 1 / sqrt(d)), cap, window: numbers, 0 for none;
+        slopes: fp32 [n_q_heads], prefix: int32 [n_seq], on the device.  Returns fp16 like q.
+        """
+        if q.dtype not in DTYPE_CODES:
+            raise ValueError("q must be fp16, bf16 or fp32")
+        n_q = [int(x) for x in n_q]
+        want = (sum(n_q), self.spec.n_q_heads, self.spec.head_dim)
+        if tuple(q.shape) != want:
+            raise ValueError(f"q must be {want}, got {tuple(q.shape)}")
+        self._on(q, "q")
+        if slopes is not None and tuple(self._on(slopes, "slopes", torch.float32).shape) != want[1:2]:
+            raise ValueError(f"slopes must be [{want[1]}]")
+        if prefix is not None and tuple(self._on(prefix, "prefix", torch.int32).shape) != (len(n_q),):
+            raise ValueError(f"prefix must be [{len(n_q)}]")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        elif self._on(out, "out", torch.float16).shape != q.shape:
+            raise ValueError("out must be shaped like q")
+        sc = KvqScores(scale, cap, window, None if slopes is None else _dev_ptr(slopes, "slopes"),
+                       None if prefix is None else _dev_ptr(prefix, "prefix"))
+        arr = (ctypes.c_int32 * len(n_q))(*n_q)
+        self._launch(stream, kvq_attend, "kvq_attend", self._h, _dev_ptr(q, "q"), DTYPE_CODES[q.dtype],
+                     arr, len(n_q), ctypes.byref(sc), _dev_ptr(out, "out"), self.workspace.data_ptr(),
+                     self.workspace.numel())
+        return out
+
+    def norm_rotary(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None, n_new,
+                    inv_freq: torch.Tensor, q_weight: torch.Tensor | None = None,
+                    k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                    positions: torch.Tensor | None = None, sections=None, interleaved: bool = False,
+                    out_dtype=torch.float16, out=None, stream=None):
+        """Norms and position rotation of new tokens' rows (kvq_norm_rotary): what ``append``,
+        ``decode`` and ``attend`` take.  Called before the append.
+
+        q, k, v: [sum(n_new), heads, d] of one type, heads side by side, any row stride (slices of
+        one projection output); inv_freq: fp32 [pairs]; q_weight, k_weight: [d] of the rows' type,
+        None for no norm; positions: None (the cache's lengths + 0, 1, ..) or int32 [rows] or
+        [axes, rows] with the pairs of each axis in ``sections``.  Returns contiguous (q, k, v) of
+        ``out_dtype`` (v None if it was), written to ``out`` if three tensors are given.
+        """
+        if q.dtype not in DTYPE_CODES or out_dtype not in DTYPE_CODES:
+            raise ValueError("rows and outputs must be fp16, bf16 or fp32")
+        n_new = [int(x) for x in n_new]
+        n, sp = sum(n_new), self.spec
+        parts = [(q, "q", sp.n_q_heads), (k, "k", sp.n_kv_heads), (v, "v", sp.n_kv_heads)]
+        strides = [0 if t is None else self._rows(self._on(t, m, q.dtype), m, n, h) for t, m, h in parts]
+        if out is None:
+            out = [None if t is None else torch.empty((n, h, sp.head_dim), dtype=out_dtype, device=t.device)
+                   for t, _, h in parts]
+        for t, o, (_, m, h) in zip((q, k, v), out, parts):
+            if (t is None) != (o is None):
+                raise ValueError(f"{m} and its output go together")
+            if o is not None and tuple(self._on(o, m + " output", out_dtype).shape) != (n, h, sp.head_dim):
+                raise ValueError(f"{m} output must be [{n}, {h}, {sp.head_dim}]")
+        for t, m in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if t is not None and tuple(self._on(t, m, q.dtype).shape) != (sp.head_dim,):
+                raise ValueError(f"{m} must be [{sp.head_dim}]")
+        if self._on(inv_freq, "inv_freq", torch.float32).dim() != 1:
+            raise ValueError("inv_freq must be [pairs]")
+        rot = KvqRotary(inv_freq=_dev_ptr(inv_freq, "inv_freq"), n_pairs=inv_freq.numel(),
+                        interleaved=int(interleaved), eps=eps,
+                        q_weight=None if q_weight is None else _dev_ptr(q_weight, "q_weight"),
+                        k_weight=None if k_weight is None else _dev_ptr(k_weight, "k_weight"))
+        if positions is not None:
+            axes = positions.shape[0] if positions.dim() == 2 else 1
+            if positions.dim() not in (1, 2) or positions.shape[-1] != n or not 1 <= axes <= 4:
+                raise ValueError(f"positions must be [{n}] or [1 to 4 axes, {n}]")
+            sections = [inv_freq.numel()] if sections is None and axes == 1 else list(sections or [])
+            if len(sections) != axes:
+                raise ValueError(f"sections must give the pairs of {axes} axes")
+            rot.positions = _dev_ptr(self._on(positions, "positions", torch.int32), "positions")
+            rot.n_axes = axes
+            rot.sections[:axes] = [int(x) for x in sections]
+        elif sections is not None:
+            raise ValueError("sections go with positions")
+        ptr = [None if t is None else t.data_ptr() for t in (q, k, v)]
+        dst = [None if t is None else _dev_ptr(t, "out") for t in out]
+        arr = (ctypes.c_int32 * len(n_new))(*n_new)
+        self._launch(stream, kvq_norm_rotary, "kvq_norm_rotary", self._h, ptr[0], strides[0], ptr[1],
+                     strides[1], ptr[2], strides[2], DTYPE_CODES[q.dtype], arr, len(n_new),
+                     ctypes.byref(rot), *dst, DTYPE_CODES[out_dtype])
+        return tuple(out)
+
+    def reorder(self, parent, shared: int = 0, stream=None):
+        """Sequence b takes over sequence ``parent[b]``, all at once (kvq_reorder); the first
+        ``shared`` tokens of moving sequences and their parents are the same already."""
+        parent = [int(x) for x in parent]
+        arr = (ctypes.c_int32 * len(parent))(*parent)
+        self._launch(stream, kvq_reorder, "kvq_reorder", self._h, arr, len(parent), int(shared))
 
     def workspace_status(self, stream=None) -> int:
         return kvq_workspace_status(self.workspace.data_ptr(), _stream(stream))

@@ -325,6 +325,101 @@ KVQ_API kvq_status kvq_decode(kvq_cache* cache, const void* q, kvq_dtype q_dtype
 KVQ_API kvq_status kvq_decode_noalloc(kvq_cache* cache, const void* q, kvq_dtype q_dtype,
                                       void* out, int32_t n_seq, void* stream);
 
+/* How kvq_attend turns q . k into a score and which keys a row sees.  All
+ * zero (or a NULL pointer to it) is the plain causal softmax. */
+typedef struct {
+  float scale;             /* multiplies q . k; 0 = 1 / sqrt(head_dim) */
+  float cap;               /* c > 0: the score is c * tanh(scale q . k / c); 0: not capped */
+  int32_t window;          /* W > 0: a row at position p sees the keys at p - W + 1 .. p; 0: 0 .. p */
+  const float* slopes;     /* device fp32 [n_q_heads] or NULL: slope_h * |p - j| is
+                              taken off the (capped) score of the key at position j */
+  const int32_t* prefix;   /* device int32 [n_seq] or NULL: every row of sequence b sees
+                              the keys at positions < prefix[b] as well, whatever the
+                              window and its own position (a prefix that is read both
+                              ways, or the first tokens beside a window) */
+} kvq_scores;
+
+/* Attention of the newest n_q[b] tokens of each sequence b < n_seq over the
+ * cache, which holds them already (kvq_append comes first): row i of
+ * sequence b is the query of the token at position p = n_b - n_q[b] + i,
+ *     out = sum_j softmax_j(s_j) v_j
+ * over the keys j that it sees (kvq_scores), with the keys and values as
+ * kvq_decode reads them.  n_q[b] = 1 is a decoding step, a few are proposed
+ * tokens checked at once, many a piece of a prompt or a new turn of a
+ * conversation.  A row that sees no key gets 0.
+ * q: device [sum_b n_q[b], n_q_heads, d], sequences concatenated in order b
+ * (fp16, bf16 or fp32, 16-byte aligned), read only; out: device, the same
+ * shape, fp16, written.  n_q: host array of n_seq counts, each at most the
+ * sequence's length (0 skips the sequence), read before the call returns;
+ * scores: host struct or NULL, read before the call returns.
+ * workspace, ws_bytes: as for kvq_decode (the same buffer serves both; calls
+ * that share it must not overlap on the GPU).
+ * The kernels read the lengths and prefix from the device, so a captured
+ * call may be replayed as appends advance them; out is then of the newest
+ * tokens at that time.  The cache's contents must be finite (as the append's
+ * are): an infinity or NaN in a key or value may reach rows that do not see it.
+ * Errors (host side): KVQ_ERR_NULL, KVQ_ERR_ARG, KVQ_ERR_CAPACITY,
+ * KVQ_ERR_EMPTY (n_q[b] > 0 on an empty sequence), KVQ_ERR_DTYPE,
+ * KVQ_ERR_ALIGN, KVQ_ERR_BUFFER_TOO_SMALL; KVQ_ERR_CUDA on launch failure. */
+KVQ_API kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype,
+                              const int32_t* n_q, int32_t n_seq, const kvq_scores* scores,
+                              void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* The norms and the position rotation of kvq_norm_rotary. */
+typedef struct {
+  const float* inv_freq;   /* device fp32 [n_pairs]: radians per position */
+  int32_t n_pairs;         /* P in [1, head_dim / 2]: the first 2P channels are rotated */
+  int32_t interleaved;     /* 0: pair i is channels (i, i + P); 1: (2i, 2i + 1) */
+  const int32_t* positions;/* device int32 [n_axes][rows], or NULL: row i of
+                              sequence b is at the cache's length of b + i */
+  int32_t n_axes;          /* 1 to 4 (with positions): e.g. time, height, width */
+  int32_t sections[4];     /* pairs of each axis, in order; their sum is P */
+  const void* q_weight;    /* device [head_dim] of the input type: query heads are
+                              normed, x / sqrt(mean(x^2) + eps) * weight; NULL: not */
+  const void* k_weight;    /* the same for the key heads */
+  float eps;               /* >= 0 */
+} kvq_rotary;
+
+/* Norms the query and key heads of n_new[b] new tokens of each sequence b <
+ * n_seq and rotates them by their positions, in one pass: what kvq_append
+ * and kvq_attend (or kvq_decode) take afterwards.  Called before the append,
+ * so that the lengths are those of the tokens before.
+ * q, k, v: device rows [sum_b n_new[b]] of n_q_heads, n_kv_heads and
+ * n_kv_heads heads of d values (dtype), a row's heads one after the other,
+ * rows q_stride, k_stride, v_stride elements apart (parts of one projection
+ * output, or arrays of their own); 16-byte aligned rows; read only.  v (with
+ * v_out) may be NULL; value heads are only converted.  q_out, k_out, v_out:
+ * device, contiguous, out_dtype, written; they must overlap neither the
+ * inputs nor each other.  n_new: host array, read before the call returns;
+ * rot: host struct.  Norm and rotation are fp32 (the angle, position times
+ * inv_freq, fp64), rounded to out_dtype once.
+ * The lengths are read on the device: a captured call may be replayed.
+ * Errors (host side): KVQ_ERR_NULL, KVQ_ERR_ARG, KVQ_ERR_CAPACITY (n_seq),
+ * KVQ_ERR_DTYPE, KVQ_ERR_ALIGN; KVQ_ERR_CUDA if the launch fails. */
+KVQ_API kvq_status kvq_norm_rotary(kvq_cache* cache, const void* q, int64_t q_stride,
+                                   const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, kvq_dtype dtype, const int32_t* n_new,
+                                   int32_t n_seq, const kvq_rotary* rot, void* q_out, void* k_out,
+                                   void* v_out, kvq_dtype out_dtype, void* stream);
+
+/* Sequence b takes over what sequence parent[b] held before the call, for
+ * every b < n_seq at once and in place: beams that follow their parents, a
+ * prompt forked into several sequences.  parent: host array of sequence
+ * numbers below max_seqs (parent[b] = b stays), read before the call
+ * returns; any map is allowed (repeats, cycles).  A sequence that takes over
+ * an empty one becomes empty.
+ * shared_tokens: the first shared_tokens tokens of every sequence that moves
+ * are the same tokens as its parent's, appended by the same calls or taken
+ * over by an earlier kvq_reorder; the groups that hold only such tokens in
+ * both are not copied.  0 copies everything.
+ * The lengths are read and updated on the device, and in the host mirror; a
+ * captured call may be replayed (kvq_sync_lengths afterwards).
+ * Errors (host side, cache unchanged): KVQ_ERR_NULL, KVQ_ERR_ARG (a parent
+ * out of range, shared_tokens above a moving sequence's or its parent's
+ * length), KVQ_ERR_CAPACITY (n_seq); KVQ_ERR_CUDA if a launch fails. */
+KVQ_API kvq_status kvq_reorder(kvq_cache* cache, const int32_t* parent, int32_t n_seq,
+                               int32_t shared_tokens, void* stream);
+
 /* fp16 decode baseline (comparison kernel; not part of the quantized path).
  * The same decode attention over an unquantized fp16 cache: k and v device
  * [n_seq][n_kv_heads][max_tokens][head_dim] fp16, 16-byte aligned; lens a

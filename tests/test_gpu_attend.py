@@ -1,0 +1,270 @@
+"""GPU parity of kvq_attend against float64 attention over the oracle's dequantized cache, within the tolerance that
+``operators_oracle.attend`` derives for every element."""
+import numpy as np
+import pytest
+import torch
+
+from asymmetric_kv_cache_b200 import inputs
+from oracle import operators_oracle as oo
+from tests import kvq_testlib as tl
+
+pytestmark = pytest.mark.gpu
+
+
+def _hist(rng, lens, hkv, d):
+    ks = [inputs.keys_channel_outliers(rng, n, hkv, d).astype(np.float16) for n in lens]
+    vs = [(inputs.values_token_norms(rng, n, hkv, d) * 3 + 0.1).astype(np.float16) for n in lens]
+    return ks, vs
+
+
+def _queries(rng, n_q, hq, d, dtype):
+    q = rng.standard_normal((sum(n_q), hq, d)).astype(np.float32)
+    return q.astype(np.float16).astype(np.float32) if dtype == "fp16" else tl.bf16_values(q) if dtype == "bf16" else q
+
+
+def _filled(spec, ks, vs, chunks=None):
+    """A cache holding the histories, appended in `chunks` (the same sizes for every sequence) or at once."""
+    cache = tl.kvq().KVQCache(spec)
+    if chunks is None:
+        tl.append_chunks(cache, ks, vs, "fp16")
+    else:
+        at = 0
+        for c in chunks:
+            tl.append_chunks(cache, [k[at:at + c] for k in ks], [v[at:at + c] for v in vs], "fp16")
+            at += c
+    return cache
+
+
+def _check(cache, spec, ks, vs, q, n_q, dtype="fp16", out=None, chunks=None, prefix=None, **kw):
+    slopes = kw.get("slopes")
+    dev = dict(kw)
+    if slopes is not None:
+        dev["slopes"] = torch.tensor(slopes, dtype=torch.float32, device="cuda")
+    if prefix is not None:
+        dev["prefix"] = torch.tensor(prefix, dtype=torch.int32, device="cuda")
+    if out is None:
+        out = cache.attend(tl.to_device(q, dtype), n_q, **dev)
+    torch.cuda.synchronize()
+    assert cache.workspace_status() == 0
+    got = out.float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    cfg, row = tl.oracle_cfg(spec), 0
+    for b, m in enumerate(n_q):
+        if m == 0:
+            continue
+        want, tol = oo.attend(cfg, ks[b], vs[b], q[row:row + m], prefix=prefix[b] if prefix is not None else 0,
+                              chunks=chunks, **kw)
+        off = np.abs(got[row:row + m] - want)
+        worst = (off / tol).max()
+        assert worst <= 1.0, (b, m, ks[b].shape[0], worst, off.max(), np.unravel_index((off / tol).argmax(), off.shape))
+        row += m
+    return out
+
+
+@pytest.mark.parametrize("kb,vb", [(4, 2), (2, 2), (4, 4), (2, 4)])
+@pytest.mark.parametrize("d,G", [(64, 32), (64, 64), (128, 32), (128, 64)])
+def test_every_layout(kb, vb, d, G):
+    """One, some and many tokens over sequences from a single token to several groups, in one call."""
+    hkv, gqa = 2, 4
+    lens = [1, 7, G, G + 1, 3 * G + 5, 2 * G, 9 * G + 31]
+    n_q = [1, 7, 3, 0, 1, 2 * G, 40]
+    spec = tl.kvq().CacheSpec(kb, vb, G, d, hkv * gqa, hkv, len(lens), 1024)
+    rng = np.random.default_rng(1000 * kb + 100 * vb + d + G)
+    ks, vs = _hist(rng, lens, hkv, d)
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, n_q, hkv * gqa, d, "fp16"), n_q)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("hkv,gqa", [(1, 1), (3, 5), (2, 8), (1, 12), (1, 20)])
+def test_head_counts_and_types(hkv, gqa, dtype):
+    lens, n_q = [70, 3, 200], [5, 3, 1]
+    spec = tl.kvq().CacheSpec(4, 2, 32, 128, hkv * gqa, hkv, 3, 256)
+    rng = np.random.default_rng(hkv * 100 + gqa)
+    ks, vs = _hist(rng, lens, hkv, 128)
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, n_q, hkv * gqa, 128, dtype), n_q, dtype)
+
+
+SCORES = [dict(cap=30.0), dict(cap=2.0), dict(window=1), dict(window=37), dict(window=64, prefix=[0, 4, 200, 70, 1]),
+          dict(prefix=[1, 1000, 64, -5, 33]), dict(slopes=True), dict(slopes=True, cap=20.0, window=50, prefix=[3, 0, 7, 0, 90]),
+          dict(scale=0.01), dict(scale=0.5, cap=10.0)]
+
+
+@pytest.mark.parametrize("kw", SCORES, ids=str)
+@pytest.mark.parametrize("d,G,R,S", [(128, 32, 0, 0), (64, 64, 48, 5), (128, 64, 16, 33)])
+def test_scores(kw, d, G, R, S):
+    hkv, gqa = 2, 4
+    lens, n_q = [1, 60, 333, 200, 500], [1, 60, 5, 150, 2]
+    kw = dict(kw)
+    if kw.pop("slopes", False):
+        kw["slopes"] = [2.0 ** -(i + 1) * (-1 if i == 5 else 1) for i in range(8)]
+    spec = tl.kvq().CacheSpec(4, 2, G, d, hkv * gqa, hkv, 5, 512, window=R, sink=S)
+    rng = np.random.default_rng(d + G + R)
+    ks, vs = _hist(rng, lens, hkv, d)
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, n_q, hkv * gqa, d, "fp16"), n_q, **kw)
+
+
+@pytest.mark.parametrize("R,S", [(16, 0), (128, 0), (1024, 0), (0, 4), (0, 40), (64, 33)])
+@pytest.mark.parametrize("G", [32, 64])
+def test_recent_and_first_tokens(R, S, G):
+    hkv, gqa, d = 2, 2, 128
+    W = R + G
+    lens = [1, max(1, S - 1), S + 1, S + R + 1, S + W - 1, S + W, S + W + 3 * G + 5]
+    n_q = [1, 1, min(S + 1, 3), 1, 9, 12, W + G]
+    spec = tl.kvq().CacheSpec(4, 2, G, d, hkv * gqa, hkv, len(lens), 2048, window=R, sink=S)
+    rng = np.random.default_rng(R + S + G)
+    ks, vs = _hist(rng, lens, hkv, d)
+    n_q = [min(a, b) for a, b in zip(n_q, lens)]
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, n_q, hkv * gqa, d, "bf16"), n_q, "bf16")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rotating_cache(d):
+    hkv, gqa = 2, 4
+    lens, n_q = [5, 100, 260], [5, 1, 70]
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, 3, 512, rotate=1, sink=4)
+    rng = np.random.default_rng(d)
+    ks, vs = _hist(rng, lens, hkv, d)
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, n_q, hkv * gqa, d, "fp16"), n_q, cap=30.0)
+
+
+@pytest.mark.parametrize("d,G,vb", [(128, 32, 2), (64, 64, 4)])
+def test_position_adaptive_widths(d, G, vb):
+    hkv, gqa, delta = 2, 4, 2 * G
+    chunks = [3 * G + 7, G, 5, 2 * G, 9 * G + 1]
+    n = sum(chunks)
+    spec = tl.kvq().CacheSpec(4, vb, G, d, hkv * gqa, hkv, 2, 2048, akvq_delta=delta)
+    rng = np.random.default_rng(G)
+    ks, vs = _hist(rng, [n, n], hkv, d)
+    n_q = [1, 50]
+    _check(_filled(spec, ks, vs, chunks), spec, ks, vs, _queries(rng, n_q, hkv * gqa, d, "fp16"), n_q, chunks=chunks)
+
+
+@pytest.mark.parametrize("n,n_q,kw", [(20000, 1, {}), (20000, 3, dict(cap=30.0)), (9000, 1, dict(window=5000, prefix=[4])),
+                                      (6000, 130, dict(window=300))])
+def test_long_sequences_are_split_and_merged(n, n_q, kw):
+    hkv, gqa, d = 2, 4, 128
+    spec = tl.kvq().CacheSpec(2, 2, 32, d, hkv * gqa, hkv, 1, 20480, window=32)
+    rng = np.random.default_rng(n + n_q)
+    ks, vs = _hist(rng, [n], hkv, d)
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, [n_q], hkv * gqa, d, "fp16"), [n_q], **kw)
+
+
+def test_many_ragged_sequences():
+    """More units than resident blocks, and more sequences than one launch takes."""
+    hkv, gqa, d = 4, 2, 64
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.integers(1, 90, size=600)]
+    n_q = [int(rng.integers(0, min(n, 4) + 1)) for n in lens]
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, len(lens), 96)
+    ks, vs = _hist(rng, lens, hkv, d)
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, n_q, hkv * gqa, d, "fp16"), n_q)
+
+
+def test_agrees_with_decode():
+    hkv, gqa, d = 8, 4, 128
+    lens = [300, 4000, 31, 1025]
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, 4, 4096)
+    rng = np.random.default_rng(9)
+    ks, vs = _hist(rng, lens, hkv, d)
+    cache = _filled(spec, ks, vs)
+    q = tl.to_device(_queries(rng, [1] * 4, hkv * gqa, d, "fp16"), "fp16")
+    a, b = cache.attend(q, [1] * 4), cache.decode(q)
+    assert (a.float() - b.float()).abs().max().item() <= tl.DECODE_TOL      # each is within it of the exact result's half
+
+
+def test_large_scores_and_equal_keys():
+    """Scores of some hundreds (one key takes all), and keys all alike (the mean of the values)."""
+    hkv, d, n = 1, 128, 150
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, 4, hkv, 2, 256)
+    rng = np.random.default_rng(5)
+    ks, vs = _hist(rng, [n, n], hkv, d)
+    ks[0] = (ks[0].astype(np.float32) * 8).astype(np.float16)
+    ks[1][:] = ks[1][:1]
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, [4, 4], 4, d, "fp16"), [4, 4])
+
+
+def test_rows_past_the_input_are_left_alone_and_zero_counts_skip():
+    spec = tl.kvq().CacheSpec(4, 2, 32, 64, 4, 1, 3, 128)
+    rng = np.random.default_rng(6)
+    ks, vs = _hist(rng, [40, 50, 60], 1, 64)
+    cache = _filled(spec, ks, vs)
+    n_q = [3, 0, 10]
+    q = _queries(rng, n_q, 4, 64, "fp16")
+    buf = torch.full((20, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    out = cache.attend(tl.to_device(q, "fp16"), n_q, out=buf[:13])
+    _check(cache, spec, ks, vs, q, n_q, out=out)
+    assert (buf[13:] == 7.0).all()
+    assert cache.attend(torch.empty((0, 4, 64), dtype=torch.float16, device="cuda"), [0, 0, 0]).shape == (0, 4, 64)
+
+
+def test_unused_tail_slots_may_hold_anything():
+    """NaN in the slots that no token has reached."""
+    spec = tl.kvq().CacheSpec(4, 2, 32, 64, 4, 1, 1, 128, window=32, sink=20)
+    rng = np.random.default_rng(7)
+    for n in (1, 19, 30, 81):
+        cache = tl.kvq().KVQCache(spec)
+        L = cache.layout
+        cache.buffer[L["blocks_offset"]:].view(torch.float16).fill_(float("nan"))
+        torch.cuda.synchronize()
+        ks, vs = _hist(rng, [n], 1, 64)
+        tl.append_chunks(cache, ks, vs, "fp16")
+        m = min(n, 12)
+        _check(cache, spec, ks, vs, _queries(rng, [m], 4, 64, "fp16"), [m])
+
+
+def test_captured_call_follows_the_lengths():
+    """append + attend captured once and replayed: out is of the newest tokens, across a group's end."""
+    hkv, gqa, d, n0, m = 2, 4, 128, 61, 3
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, 2, 256)
+    rng = np.random.default_rng(8)
+    steps = 5
+    ks, vs = _hist(rng, [n0 + m * (steps + 1)] * 2, hkv, d)
+    cache = _filled(spec, [k[:n0] for k in ks], [v[:n0] for v in vs])
+    prefix = torch.tensor([2, 0], dtype=torch.int32, device="cuda")
+    q = torch.zeros((2 * m, hkv * gqa, d), dtype=torch.float16, device="cuda")
+    kin, vin = (torch.zeros((2 * m, hkv, d), dtype=torch.float16, device="cuda") for _ in range(2))
+    out = torch.zeros_like(q)
+    feed = lambda i: [tl.to_device(np.concatenate([x[b][n0 + i * m:n0 + (i + 1) * m] for b in range(2)]), "fp16")  # noqa: E731
+                      for x in (ks, vs)]
+
+    def step():
+        cache.append(kin, vin, [m, m])
+        cache.attend(q, [m, m], window=40, prefix=prefix, out=out)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):               # a first, eager step
+        kin.copy_(feed(0)[0]), vin.copy_(feed(0)[1])
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for i in range(1, steps + 1):
+        x = _queries(rng, [m, m], hkv * gqa, d, "fp16")
+        q.copy_(tl.to_device(x, "fp16"))
+        kin.copy_(feed(i)[0]), vin.copy_(feed(i)[1])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        n = n0 + (i + 1) * m
+        got = out.clone()
+        _check(cache, spec, [k[:n] for k in ks], [v[:n] for v in vs], x, [m, m], out=got, window=40, prefix=[2, 0])
+
+
+def test_python_refusals():
+    K = tl.kvq()
+    cache = K.KVQCache(K.CacheSpec(4, 2, 32, 64, 4, 1, 2, 64))
+    cache.append(*(torch.zeros((5, 1, 64), dtype=torch.float16, device="cuda") for _ in range(2)), [5])
+    q = torch.zeros((2, 4, 64), dtype=torch.float16, device="cuda")
+    f, i = (torch.zeros(4, dtype=t, device="cuda") for t in (torch.float32, torch.int32))
+    for bad in (lambda: cache.attend(q.double(), [2]), lambda: cache.attend(q, [1]), lambda: cache.attend(q.cpu(), [2]),
+                lambda: cache.attend(q.transpose(0, 1).contiguous().transpose(0, 1), [2]),
+                lambda: cache.attend(q, [2], slopes=f[:3]), lambda: cache.attend(q, [2], slopes=f.half()),
+                lambda: cache.attend(q, [2], prefix=i), lambda: cache.attend(q, [2], prefix=i[:1].long()),
+                lambda: cache.attend(q, [2], out=q.float()), lambda: cache.attend(q, [2], out=q[:1]),
+                lambda: cache.attend(q, [2], prefix=i[:1].cpu())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: cache.attend(q, [2], cap=-1.0), lambda: cache.attend(q, [1, 1]), lambda: cache.attend(q, [2], window=-3)):
+        with pytest.raises(K.KvqError):
+            bad()

@@ -28,7 +28,7 @@ struct kvq_cache {
   size_t buf_bytes;
   std::vector<int32_t> lens;   // host mirror of the device lengths
   int max_ctas[2];             // decode CTA caps, narrow / wide (0 until queried)
-  int attend_ctas;             // resident attend CTAs (0 until queried)
+  int attend_ctas[2];          // resident attend CTAs, register / tensor-core tiles (0 until queried)
 };
 
 namespace {
@@ -174,7 +174,7 @@ kvq_status kvq_cache_required_bytes(const kvq_config* cfg, size_t* cache_bytes,
   kvq::Geom g;
   kvq::make_geom(*cfg, &g);
   kvq::WsLayout w;
-  kvq::make_ws_layout(g, &w);
+  kvq::make_cache_ws_layout(g, &w);
   if (cache_bytes) *cache_bytes = (size_t)g.total_bytes;
   if (workspace_bytes) *workspace_bytes = (size_t)w.total;
   return ok();
@@ -201,12 +201,12 @@ kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_buf, size_t bytes, 
   c->cfg = *cfg;
   c->cfg.layout_version = KVQ_LAYOUT_VERSION;
   c->geom = g;
-  kvq::make_ws_layout(g, &c->ws);
+  kvq::make_cache_ws_layout(g, &c->ws);
   c->buf = static_cast<unsigned char*>(dev_buf);
   c->buf_bytes = bytes;
   c->lens.assign(cfg->max_seqs, 0);
   c->max_ctas[0] = c->max_ctas[1] = 0;
-  c->attend_ctas = 0;
+  c->attend_ctas[0] = c->attend_ctas[1] = 0;
   *out = c;
   return ok();
 }
@@ -450,8 +450,12 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   if ((int64_t)ws_bytes < cache->ws.total)
     return fail(KVQ_ERR_BUFFER_TOO_SMALL, "workspace has %zu bytes, needs %lld", ws_bytes,
                 (long long)cache->ws.total);
-  if (cache->attend_ctas == 0) {
-    cudaError_t e = kvq::attend_max_ctas(g, &cache->attend_ctas);
+  if (cache->attend_ctas[0] == 0) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+      e = cudaDeviceGetAttribute(&cache->attend_ctas[1], cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = kvq::attend_max_ctas(g, &cache->attend_ctas[0]);
     if (e != cudaSuccess) return cuda_fail(e, "attend occupancy");
   }
   kvq::AttendArgs a = {};
@@ -465,15 +469,21 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   a.score_window = sc.window;
   a.slopes = sc.slopes;
   a.prefix = sc.prefix;
+  // fp32 and rotated queries are not fp16 numbers: value and residual parts
+  a.residual = q_dtype == KVQ_FP32 || g.rotate;
   static thread_local kvq::AttendSeqs seqs;
   int64_t row = 0;
   for (int s0 = 0; s0 < n_seq; s0 += kvq::kAttendMaxSeqs) {
     const int n = std::min(kvq::kAttendMaxSeqs, n_seq - s0);
-    const bool split = kvq::plan_attend(g, cache->lens.data(), n_q, s0, n, sc.window,
-                                        cache->attend_ctas, &row, &seqs);
-    if (seqs.piece_off[n] == 0) continue;
-    cudaError_t e = kvq::launch_attend(g, cache->ws, a, seqs, split, (cudaStream_t)stream);
-    if (e != cudaSuccess) return cuda_fail(e, "attend launch");
+    for (int tc = 1; tc >= 0; --tc) {
+      const int unit_rows = !tc ? kvq::kAttendRows : a.residual ? 128 : 256;
+      const bool split = kvq::plan_attend(g, cache->lens.data(), n_q, s0, n, sc.window,
+                                          cache->attend_ctas[tc], unit_rows, row, &seqs);
+      if (seqs.piece_off[n] == 0) continue;
+      cudaError_t e = kvq::launch_attend(g, cache->ws, a, seqs, split, (cudaStream_t)stream);
+      if (e != cudaSuccess) return cuda_fail(e, "attend launch");
+    }
+    for (int i = 0; i < n; ++i) row += n_q[s0 + i];
   }
   return ok();
 }

@@ -8,10 +8,10 @@ namespace {
 
 constexpr int kMergeThreads = 32 * kAttendRows;
 
-// Merges the pieces of split units: a block per piece, of which the first
-// piece of each unit does the work (the others leave at once), a warp per
-// row.  With the rows' maxima m_i and sums l_i relative to them, out = sum_i
-// 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// Merges the pieces of split units, a warp per row: blocks are (piece, eight
+// rows of the unit), of which those of a unit's first piece do the work (the
+// others leave at once).  With the rows' maxima m_i and sums l_i relative to
+// them, out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     attend_merge_kernel(const Geom g, const WsLayout w, const AttendArgs a, const AttendSeqs seqs) {
@@ -23,14 +23,17 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int mid = (lo + hi) >> 1;
     if (seqs.piece_off[mid] <= (int)blockIdx.x) lo = mid; else hi = mid;
   }
-  const int R = seqs.n_q[lo] * g.gqa, tiles = (R + kAttendRows - 1) / kAttendRows;
+  const int R = seqs.n_q[lo] * g.gqa, tiles = (R + seqs.unit_rows - 1) / seqs.unit_rows;
   const int local = blockIdx.x - seqs.piece_off[lo];
   const int parts = (seqs.piece_off[lo + 1] - seqs.piece_off[lo]) / (g.hkv * tiles);
-  const int h = local / parts / tiles, r = local / parts % tiles * kAttendRows + warp;
+  const int h = local / parts / tiles, tile = local / parts % tiles;
+  const int ur = blockIdx.y * kAttendRows + warp;        // row of the unit
+  // (the tensor-core kernel numbers a sequence's row tiles from the last)
+  const int r = (seqs.unit_rows == kAttendRows ? tile : tiles - 1 - tile) * seqs.unit_rows + ur;
   if (parts < 2 || local % parts != 0 || r >= R) return;
   const float* ps = reinterpret_cast<const float*>(a.ws + w.partials_off) +
-                    ((int64_t)blockIdx.x * kAttendRows + warp) * (D + 4);
-  constexpr int64_t kStep = (int64_t)kAttendRows * (D + 4);
+                    ((int64_t)blockIdx.x * seqs.slot_rows + ur) * (D + 4);
+  const int64_t kStep = (int64_t)seqs.slot_rows * (D + 4);
   float m = -INFINITY;
   for (int s = lane; s < parts; s += 32) m = fmaxf(m, ps[s * kStep + D]);
 #pragma unroll
@@ -71,7 +74,7 @@ cudaError_t launch_attend(const Geom& g, const WsLayout& w, const AttendArgs& a,
 #undef KVQ_CASE
   if (e != cudaSuccess || !split) return e;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)s.piece_off[s.n]);
+  lc.gridDim = dim3((unsigned)s.piece_off[s.n], (unsigned)((s.slot_rows + kAttendRows - 1) / kAttendRows));
   lc.blockDim = dim3(kMergeThreads);
   lc.stream = stream;
   cudaLaunchAttribute la[1];

@@ -1,6 +1,6 @@
-// Instantiations of the attend kernel for head_dim 128, group 32, 2-bit
+// Instantiations of the attend kernels for head_dim 128, group 32, 2-bit
 // values (2- and 4-bit keys).
-#include "kvq_attend_kernels.cuh"
+#include "kvq_attend_tc.cuh"
 
 namespace kvq {
 KVQ_ATTEND_DEFINE(128, 4, 2, 32)

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kAttThreads, 4)
     }
     if (parts > 1) {
       float* ps = reinterpret_cast<float*>(a.ws + w.partials_off) +
-                  ((int64_t)blockIdx.x * kAttendRows + r) * (D + 4);
+                  ((int64_t)blockIdx.x * seqs.slot_rows + r) * (D + 4);
 #pragma unroll
       for (int i = 0; i < V; ++i) ps[lane * V + i] = y[i];
       if (lane == 0) {
@@ -544,21 +544,5 @@ cudaError_t attend_occupancy(int* out) {
   *out = sms * (per > 0 ? per : 1);
   return e;
 }
-
-#define KVQ_ATTEND_DEFINE(D_, KB_, VB_, G_)                                                       \
-  cudaError_t attend_max_ctas_##D_##_##KB_##_##VB_##_##G_(int* out) {                             \
-    return attend_occupancy<D_, KB_, VB_, G_>(out);                                               \
-  }                                                                                               \
-  cudaError_t launch_attend_##D_##_##KB_##_##VB_##_##G_(const Geom& g, const WsLayout& w,         \
-                                                        const AttendArgs& a, const AttendSeqs& s, \
-                                                        cudaStream_t stream) {                    \
-    using C = AttCfg<D_, KB_, VB_, G_>;                                                           \
-    if (g.block_bytes != C::BLK) return cudaErrorInvalidValue;                                    \
-    cudaError_t e = attend_configure<D_, KB_, VB_, G_>();                                         \
-    if (e != cudaSuccess) return e;                                                               \
-    attend_kernel<D_, KB_, VB_, G_>                                                               \
-        <<<(unsigned)s.piece_off[s.n], kAttThreads, C::SMEM, stream>>>(g, w, a, s);               \
-    return cudaGetLastError();                                                                    \
-  }
 
 }  // namespace kvq

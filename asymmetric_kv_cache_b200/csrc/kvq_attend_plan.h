@@ -8,42 +8,61 @@
 
 namespace kvq {
 
-// The launch of sequences [s0, s0 + n): `row` counts the call's query rows.
-// A unit is (sequence, kv head, tile of kAttendRows rows).  With at least as
+// The launch of sequences [s0, s0 + n), of which those with at least
+// kAttendTcRows rows per kv head belong to the tensor-core kernel (unit_rows >
+// kAttendRows) and the others to the register-tile kernel; the launch of
+// either kernel skips the other's.  row0: the first sequence's first query
+// row.
+//
+// A unit is (sequence, kv head, tile of unit_rows rows).  With at least as
 // many units as resident CTAs every unit is one piece.  Otherwise the units
 // are cut into about max_ctas pieces, a sequence's units in proportion to
-// the keys that they see, and into no more pieces than a CTA's warps have
-// blocks for.  The lengths are the host's; the kernel cuts what it finds in
-// the device's into the same number of pieces, so a replayed launch stays
-// right when they have grown.  Returns whether some unit is cut.
+// the keys that they see, into no pieces of fewer than four steps, and into
+// no more than the partials have room for.  The lengths are the host's; the
+// kernels cut what they find in the device's into the same number of pieces,
+// so a replayed launch stays right when they have grown.  Returns whether
+// some unit is cut.
 inline bool plan_attend(const Geom& g, const int32_t* lens, const int32_t* n_q, int s0, int n,
-                        int score_window, int max_ctas, int64_t* row, AttendSeqs* out) {
+                        int score_window, int max_ctas, int unit_rows, int64_t row0,
+                        AttendSeqs* out) {
   out->n = n;
   out->seq0 = s0;
-  int64_t units = 0, cost = 0;
-  auto tiles = [&](int b) { return ((int64_t)n_q[b] * g.gqa + kAttendRows - 1) / kAttendRows; };
-  auto blocks = [&](int b) {
-    int64_t keys = lens[b];
-    if (score_window > 0) keys = std::min<int64_t>(keys, (int64_t)score_window + kAttendRows / g.gqa + g.G);
-    return keys / g.G + 1;
+  out->unit_rows = unit_rows;
+  out->slot_rows = kAttendRows;
+  const bool tc = unit_rows > kAttendRows;
+  const int step = tc ? 64 : g.G;        // keys of one step of the kernel
+  auto rows = [&](int b) {
+    const int64_t r = (int64_t)n_q[b] * g.gqa;
+    return tc == (r >= kAttendTcRows) ? r : 0;
   };
+  auto tiles = [&](int b) { return (rows(b) + unit_rows - 1) / unit_rows; };
+  auto steps = [&](int b) {
+    int64_t keys = lens[b];
+    if (score_window > 0) keys = std::min<int64_t>(keys, (int64_t)score_window + unit_rows / g.gqa + step);
+    return keys / step + 1;
+  };
+  int64_t units = 0, cost = 0;
   for (int b = s0; b < s0 + n; ++b) {
     const int64_t u = g.hkv * tiles(b);
     units += u;
-    cost += u * blocks(b);
+    cost += u * steps(b);
+    if (u > 0)
+      out->slot_rows = (int)std::max<int64_t>(
+          out->slot_rows, (std::min<int64_t>(rows(b), unit_rows) + kAttendRows - 1) / kAttendRows * kAttendRows);
   }
-  int64_t pieces = 0;
+  const int64_t want = std::min<int64_t>(max_ctas, kAttendPartialRows / out->slot_rows - units);
+  int64_t pieces = 0, row = row0;
   bool split = false;
   for (int i = 0; i < n; ++i) {
     const int b = s0 + i;
-    out->row_off[i] = (int32_t)*row;
+    out->row_off[i] = (int32_t)row;
     out->n_q[i] = n_q[b];
     out->piece_off[i] = (int32_t)pieces;
-    *row += n_q[b];
+    row += n_q[b];
     int64_t parts = 1;
-    if (units < max_ctas && n_q[b] > 0) {
-      parts = blocks(b) * max_ctas / cost;
-      parts = std::max<int64_t>(1, std::min(parts, (blocks(b) + 3) / 4));
+    if (units < want && tiles(b) > 0) {
+      parts = steps(b) * want / cost;
+      parts = std::max<int64_t>(1, std::min(parts, (steps(b) + 3) / 4));
       split |= parts > 1;
     }
     pieces += g.hkv * tiles(b) * parts;

@@ -1,0 +1,666 @@
+// kvq_attend for many rows per kv head, on the 5th-generation tensor cores.
+//
+// The same attention as attend_kernel.  Unit: (sequence, kv head, 256 of the
+// kv head's n_q * gqa rows) = two row tiles A and B of M = 128, one CTA per
+// unit (per part of its key list, when there are few units).  Keys come in
+// tiles of 64 tokens that both row tiles use:
+//   * 4 warps turn the codes into operands in shared memory: k = s code + z
+//     as an fp16 value K1 and the fp16 residual K2 of the exact number (the
+//     product's by a fused multiply-subtract, the sum's by the error-free
+//     two-sum), v = s code + z rounded to fp16 once.  The codes' storage
+//     order is the order of the operand's 8 x 16-byte core matrices, a lane's
+//     pair per core row, so every 32-lane store is one core matrix.
+//   * one thread issues S = Q K1^T + Q K2^T (Q as A operand in tensor memory:
+//     from shared memory it would take the bandwidth that K needs, 128 + 64
+//     bytes a cycle of 128) and O += P V (P in tensor memory, over S).
+//   * 4 warps per row tile, a thread per row, turn S into P: no exchange
+//     between threads.  The maximum that the weights refer to is only moved
+//     when a score passes it by 2^8, so O in tensor memory is rarely
+//     rescaled; weights stay below 2^8 and the sum is fp32.
+// Rows of fp32 or rotated queries, which fp16 does not hold exactly, come as
+// value and residual in the two Q areas, one row tile per unit, and S gets
+// the third product Q2 K1^T.
+#pragma once
+
+#include "kvq_attend_kernels.cuh"
+
+namespace kvq {
+
+constexpr int kTcRows = 256;              // rows of a unit (kTcRows / 2 with residuals)
+constexpr int kTcKeys = 64;               // keys of a tile
+constexpr int kTcWarps = 13;              // 4 + 4 softmax, 4 operands, 1 issue
+constexpr int kTcThreads = 32 * kTcWarps;
+constexpr float kTcSlack = 8.f;           // a maximum may be passed by 2^8 before O is rescaled
+
+template <int D>
+struct TcAtt {
+  static constexpr int K_BYTES = kTcKeys * D * 2;        // K1, K2, V each
+  static constexpr int STAGE = 3 * K_BYTES;
+  static constexpr int NST = D == 128 ? 4 : 6;
+  // the query's rows on their way in, and the result's on their way out, use
+  // the stages before and after the tiles: per softmax warp 32 padded rows
+  static constexpr int IO_ROW = 4 * D + 16;
+  static constexpr int IO_BYTES = 8 * 32 * IO_ROW;
+  static constexpr int AREA = NST * STAGE > IO_BYTES ? NST * STAGE : IO_BYTES;
+  static constexpr int BAR = AREA;
+  // barriers: full[NST], empty[NST], s_full[2], p_full[2], pv_done[2]
+  static constexpr int B_FULL = 0, B_EMPTY = NST, B_S = 2 * NST, B_P = B_S + 2, B_PV = B_P + 2,
+                       NBAR = B_PV + 2;
+  static constexpr int SMEM = BAR + NBAR * 8;
+  // tensor memory columns
+  static constexpr uint32_t T_S = 0, T_Q = 128, T_O = 128 + D, T_COLS = 512;
+  static_assert(T_O + 2 * D <= T_COLS, "tensor memory");
+};
+
+__device__ __forceinline__ void att_tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void att_tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void att_tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+// D (tensor memory) (+)= A (tensor memory) * B (shared-memory descriptor)
+__device__ __forceinline__ void att_tc_mma(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ bool att_elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n.reg .pred e;\n.reg .b32 r;\nelect.sync r|e, 0xffffffff;\nselp.u32 %0, 1, 0, e;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void att_tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void att_tc_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// 32 columns of this warp's 32 lanes
+__device__ __forceinline__ void att_tc_ld32(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+}
+#define KVQ_R4(b) "r"(r[b]), "r"(r[b + 1]), "r"(r[b + 2]), "r"(r[b + 3])
+__device__ __forceinline__ void att_tc_st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      KVQ_R4(0), KVQ_R4(4), KVQ_R4(8), KVQ_R4(12), KVQ_R4(16), KVQ_R4(20), KVQ_R4(24), KVQ_R4(28)
+      : "memory");
+}
+#undef KVQ_R4
+// K-major operand of contiguous core matrices (8 rows x 16 bytes): those of
+// neighbouring K eights 128 bytes apart, of neighbouring row eights sbo bytes.
+__device__ __forceinline__ uint64_t att_tc_desc(uint32_t saddr, uint32_t sbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+// fp16 operands, both K-major, fp32 accumulator, M = 128
+__host__ __device__ constexpr uint32_t att_tc_idesc(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// Bounded wait (2^14 tries that sleep up to 20 us each in hardware); a wait
+// that runs out clears the warp's `ok` and is recorded.
+__device__ __forceinline__ void att_tc_wait(uint64_t* bar, uint32_t parity, bool& ok, int32_t* err,
+                                            int lane) {
+  if (!ok) return;
+  bool got = false;
+  for (int it = 0; it < (1 << 14) && !got; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    got = done != 0;
+  }
+  if (!__all_sync(0xffffffffu, got)) {
+    ok = false;
+    if (lane == 0) atomicExch(err, KVQ_ERR_DEVICE);
+  }
+}
+
+__device__ __forceinline__ uint32_t hadd2_b(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub2_b(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+template <int N>
+__device__ __forceinline__ void ldg_words(const void* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x; w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  }
+}
+
+// Operands of 16 tokens (16-token part `sub` of the 32 tokens hf of a block):
+// token eights te, te + 1 of the tile.  `wait` is called between the loads
+// and the stores.
+template <int D, int KBL, int VB, int G, class Wait>
+__device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, int sub,
+                                              unsigned char* stage, int te, int lane,
+                                              const Wait& wait) {
+  constexpr int P = D / 8, MT = D / 16, J = D / G;
+  constexpr int LBK = D * KBL / 32, WK = LBK / 4, FK = 16 / KBL;
+  constexpr int WV = D * VB / 64, FV = 16 / VB;
+  constexpr int OFF_S = G * D * KBL / 8, OFF_Z = OFF_S + 2 * D, OFF_V = OFF_Z + 2 * D,
+                OFF_VS = OFF_V + G * D * VB / 8, OFF_VZ = OFF_VS + 2 * G * J;
+  const int i4 = lane & 3, kv = 2 * hf + sub;
+  uint32_t kw[2][WK], ks[P], kz[P], vw[WV], vs[2 * J], vz[2 * J];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) ldg_words<WK>(blk + ((2 * kv + x) * 32 + lane) * LBK, kw[x]);
+  ldg_words<P>(blk + OFF_S + i4 * (D / 2), ks);
+  ldg_words<P>(blk + OFF_Z + i4 * (D / 2), kz);
+  ldg_words<WV>(blk + OFF_V + (kv * 32 + lane) * (4 * WV), vw);
+  ldg_words<2 * J>(blk + OFF_VS + (4 * kv + i4) * J * 8, vs);
+  ldg_words<2 * J>(blk + OFF_VZ + (4 * kv + i4) * J * 8, vz);
+  wait();
+  unsigned char* k1 = stage + te * P * 128 + lane * 4;
+  unsigned char* v1 = stage + 2 * TcAtt<D>::K_BYTES + te * 128 + lane * 4;
+  static_for<P>([&](auto pc) {
+    constexpr int p = decltype(pc)::value;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t c = unpack_pair<KBL, p % FK>(kw[x][p / FK]);
+      const uint32_t h = hmul2_b(c, ks[p]), e = hfma2_negc_b(c, ks[p], h);   // c s = h + e
+      const uint32_t hi = hadd2_b(h, kz[p]), b = hsub2_b(hi, h);             // h + z = hi + f
+      const uint32_t f = hadd2_b(hsub2_b(h, hsub2_b(hi, b)), hsub2_b(kz[p], b));
+      *reinterpret_cast<uint32_t*>(k1 + (x * P + p) * 128) = hi;
+      *reinterpret_cast<uint32_t*>(k1 + TcAtt<D>::K_BYTES + (x * P + p) * 128) = hadd2_b(e, f);
+    }
+  });
+  static_for<MT>([&](auto mc) {
+    constexpr int mt = decltype(mc)::value;
+    constexpr int j = 16 * mt / G, w = mt / (FV / 4), u = mt % (FV / 4);
+    static_for<4>([&](auto qc) {
+      constexpr int hr = decltype(qc)::value & 1, kh = decltype(qc)::value >> 1;
+      *reinterpret_cast<uint32_t*>(v1 + ((2 * mt + hr) * (kTcKeys / 8) + kh) * 128) = hfma2_b(
+          unpack_pair<VB, 2 * u + hr + FV / 2 * kh>(vw[w]), vs[2 * j + kh], vz[2 * j + kh]);
+    });
+  });
+}
+
+// The same for 16 fp16 tokens, `valid` of which hold tokens (0 for a part
+// that is not there: k and v are not read then).
+template <int D, class Wait>
+__device__ __forceinline__ void tc_fill_fp16(const __half* k, const __half* v, int valid,
+                                             unsigned char* stage, int te, int lane,
+                                             const Wait& wait) {
+  constexpr int P = D / 8, MT = D / 16;
+  const int g8 = lane >> 2, i4 = lane & 3;
+  const uint32_t* kw = reinterpret_cast<const uint32_t*>(k);
+  const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
+  wait();
+  unsigned char* k1 = stage + te * P * 128 + lane * 4;
+  unsigned char* v1 = stage + 2 * TcAtt<D>::K_BYTES + te * 128 + lane * 4;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const bool there = 8 * x + g8 < valid;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      *reinterpret_cast<uint32_t*>(k1 + (x * P + p) * 128) =
+          there ? kw[(8 * x + g8) * (D / 2) + 4 * p + i4] : 0u;
+      *reinterpret_cast<uint32_t*>(k1 + TcAtt<D>::K_BYTES + (x * P + p) * 128) = 0u;
+    }
+  }
+#pragma unroll
+  for (int kh = 0; kh < 2; ++kh) {
+    const int t = 8 * kh + 2 * i4;
+    const uint32_t keep = (t < valid ? 0x0000FFFFu : 0u) | (t + 1 < valid ? 0xFFFF0000u : 0u);
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m)
+      *reinterpret_cast<uint32_t*>(v1 + (m * (kTcKeys / 8) + kh) * 128) =
+          keep ? vw[(4 * kh + i4) * D + 8 * m + g8] & keep : 0u;
+  }
+}
+
+// The visible keys of a unit as a list of 32-token parts: blocks, then the
+// sink, then the tail.
+struct TcKeys {
+  int S, N, T, G, per, gA, gB, nblk, nsink, parts;
+  __device__ __forceinline__ int group(int c) const {
+    const int it = c / per;
+    return it < gA ? it : gB + it - gA;
+  }
+  // first position and number of tokens (0: no such part)
+  __device__ __forceinline__ void at(int c, int* pos, int* valid) const {
+    if (c < nblk * per) {
+      *pos = S + group(c) * G + 32 * (c % per);
+      *valid = 32;
+    } else if (c < nblk * per + nsink) {
+      *pos = 32 * (c - nblk * per);
+      *valid = min(32, S - *pos);
+    } else {
+      const int t = 32 * (c - nblk * per - nsink);
+      *pos = N + t;
+      *valid = c < parts ? min(32, T - t) : 0;
+    }
+  }
+};
+
+template <int D, int KB, int VB, int G>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attend_tc_kernel(const Geom g, const WsLayout w, const AttendArgs a, const AttendSeqs seqs) {
+  using C = TcAtt<D>;
+  extern __shared__ __align__(1024) unsigned char att_tc_smem[];
+  unsigned char* const smem = att_tc_smem;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR);
+  __shared__ uint32_t tmem_base;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t* err = reinterpret_cast<int32_t*>(a.ws + w.err_off);
+
+  // ---- this piece
+  int sq;
+  {
+    int lo = 0, hi = seqs.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (seqs.piece_off[mid] <= (int)blockIdx.x) lo = mid; else hi = mid;
+    }
+    sq = lo;
+  }
+  const int unit_rows = seqs.unit_rows;
+  const bool exact = a.residual != 0;      // value and residual areas for one row tile
+  const int nq = seqs.n_q[sq], R = nq * g.gqa;
+  const int tiles = (R + unit_rows - 1) / unit_rows;
+  const int local = blockIdx.x - seqs.piece_off[sq];
+  const int parts = (seqs.piece_off[sq + 1] - seqs.piece_off[sq]) / (g.hkv * tiles);
+  const int part = local % parts, h = local / parts / tiles;
+  const int tile = tiles - 1 - local / parts % tiles;     // the longest key lists first
+  const int r0 = tile * unit_rows, nr = min(unit_rows, R - r0);
+  const int nx = nr > 128 ? 2 : 1;         // row tiles in use
+  const int seq = seqs.seq0 + sq;
+  const int n = min(max(reinterpret_cast<const int32_t*>(a.cache + g.lens_off)[seq], 0), g.max_tokens);
+
+  const int ng = quantized_groups_s(n, G, g.window, g.sink);
+  const int window = a.score_window > 0 ? a.score_window : 0x7fffffff;
+  const int prefix = a.prefix ? min(max(a.prefix[seq], 0), n) : 0;
+  const int p_lo = n - nq + r0 / g.gqa, p_hi = n - nq + (r0 + nr - 1) / g.gqa;
+  const int first = max(0, p_lo >= window ? p_lo - window + 1 : 0);
+  TcKeys keys;
+  keys.G = G;
+  keys.per = G / 32;
+  keys.S = min(n, g.sink);
+  keys.N = keys.S + ng * G;
+  keys.T = n - keys.N;
+  {
+    const int gA0 = min(ng, max(0, (prefix - keys.S + G - 1) / G));
+    keys.gB = min(ng, max(0, first - keys.S) / G);
+    const int gC = max(gA0, min(ng, max(0, (p_hi + 1 - keys.S + G - 1) / G)));
+    keys.gA = min(gA0, keys.gB);
+    keys.nblk = keys.gA + max(0, gC - keys.gB);
+  }
+  keys.nsink = (keys.S + 31) / 32;
+  keys.parts = keys.nblk * keys.per + keys.nsink + (keys.T + 31) / 32;
+  const int all_tiles = (keys.parts + 1) / 2;
+  const int t0 = (int)((int64_t)all_tiles * part / parts), t1 = (int)((int64_t)all_tiles * (part + 1) / parts);
+  const int nt = t1 - t0;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(&bars[C::B_FULL + s], 4);
+      mbar_init(&bars[C::B_EMPTY + s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars[C::B_S + x], 1);
+      mbar_init(&bars[C::B_P + x], 4);
+      mbar_init(&bars[C::B_PV + x], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_base)),
+                 "r"(C::T_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // ---- query rows: each softmax warp brings its 32 rows through its part of
+  // the stages (rotated where the cache is), then a thread per row
+  const int X = warp >> 2, wrow = 128 * X + 32 * (warp & 3);     // row tile, the warp's first row
+  unsigned char* io = smem + (warp & 7) * 32 * C::IO_ROW;
+  if (warp < 8 && X < nx) {
+    constexpr int V = D / 32;
+    for (int i = 0; i < 32; ++i) {
+      const int r = r0 + wrow + i;
+      float y[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) y[k] = 0.f;
+      if (wrow + i < nr) {
+        const int64_t at = ((int64_t)(seqs.row_off[sq] + r / g.gqa) * g.hq + h * g.gqa + r % g.gqa) * D + lane * V;
+#pragma unroll
+        for (int k = 0; k < V; ++k) y[k] = load_as_float(a.q, at + k, a.q_dtype);
+      }
+      if (g.rotate) {
+        fwht_lanes<D, V>(y, lane);
+#pragma unroll
+        for (int k = 0; k < V; ++k) y[k] *= rot_scale<D>();
+      }
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        const uint32_t hi = pack_h2(y[k], y[k + 1]);
+        const float2 f = __half22float2(u32_as_h2(hi));
+        uint32_t* dst = reinterpret_cast<uint32_t*>(io + i * C::IO_ROW) + (lane * V + k) / 2;
+        dst[0] = hi;
+        dst[D / 2] = pack_h2(y[k] - f.x, y[k + 1] - f.y);
+      }
+    }
+  }
+  att_tc_fence_before();
+  __syncthreads();
+  att_tc_fence_after();
+  const uint32_t tm = tmem_base;
+  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+  if (warp < 8 && X < nx) {
+    const uint4* src = reinterpret_cast<const uint4*>(io + lane * C::IO_ROW);
+    for (int x = 0; x < (exact ? 2 : 1); ++x) {
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = src[x * (D / 8) + 8 * c + i];
+          r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
+        }
+        att_tc_st32(tm + lanes + C::T_Q + (X + x) * (D / 2) + 32 * c, r);
+      }
+    }
+    att_tc_wait_st();
+  }
+  att_tc_fence_before();
+  __syncthreads();          // Q is in tensor memory, the stages are free
+  att_tc_fence_after();
+
+  bool ok = true;
+  if (warp < 8) {
+    if (X < nx) {
+      // ================= softmax: a thread per row =================
+      const int r = wrow + lane, rc = min(r, nr - 1);
+      RowRule rr;
+      rr.pos = n - nq + (r0 + rc) / g.gqa;
+      rr.prefix = prefix;
+      rr.window = window;
+      rr.scale2 = a.scale * kLog2e;
+      rr.cap2 = a.cap * kLog2e;
+      rr.inv_cap2 = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+      rr.slope2 = a.slopes ? a.slopes[h * g.gqa + (r0 + rc) % g.gqa] * kLog2e : 0.f;
+      // positions of this warp's rows
+      const int w_lo = n - nq + (r0 + min(wrow, nr - 1)) / g.gqa;
+      const int w_hi = n - nq + (r0 + min(wrow + 31, nr - 1)) / g.gqa;
+      const bool plain = a.cap == 0.f && !a.slopes;
+      float m = -INFINITY, l = 0.f;
+      const uint32_t ts = tm + lanes + C::T_S + kTcKeys * X, to = tm + lanes + C::T_O + D * X;
+      for (int t = 0; t < nt; ++t) {
+        att_tc_wait(&bars[C::B_S + X], t & 1, ok, err, lane);
+        if (!ok) break;
+        att_tc_fence_after();
+        float s[kTcKeys];
+        att_tc_ld32(ts, reinterpret_cast<uint32_t*>(s));
+        att_tc_ld32(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
+        att_tc_wait_ld();
+        float mul = rr.scale2;
+        bool easy = plain;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          int pos, valid;
+          keys.at(2 * (t0 + t) + c, &pos, &valid);
+          const bool every = valid == 32 && (pos + 32 <= prefix || (pos + 31 <= w_lo && w_hi - pos < window));
+          easy = easy && every;
+        }
+        if (!easy) {
+          mul = 1.f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            int pos, valid;
+            keys.at(2 * (t0 + t) + c, &pos, &valid);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = att_score(rr, s[32 * c + i], pos + i);
+              s[32 * c + i] = i < valid && att_visible(rr, pos + i) ? x : -INFINITY;
+            }
+          }
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int i = 1; i < kTcKeys; ++i) mx = fmaxf(mx, s[i]);
+        mx *= mul;
+        if (__any_sync(0xffffffffu, mx > m + kTcSlack)) {
+          const float mn = fmaxf(m, mx);
+          const float alpha = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
+          m = mn;
+          l *= alpha;
+          if (t > 0) {
+            att_tc_wait(&bars[C::B_PV + X], (t - 1) & 1, ok, err, lane);
+            if (!ok) break;
+            att_tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              att_tc_ld32(to + 32 * c, o);
+              att_tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              att_tc_st32(to + 32 * c, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        uint32_t p[kTcKeys / 2];
+#pragma unroll
+        for (int i = 0; i < kTcKeys; i += 2) {
+          const float p0 = fast_exp2(fmaf(s[i], mul, -base)), p1 = fast_exp2(fmaf(s[i + 1], mul, -base));
+          l += p0 + p1;
+          p[i / 2] = pack_h2(p0, p1);
+        }
+        att_tc_st32(ts, p);
+        att_tc_wait_st();
+        att_tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::B_P + X]);
+      }
+      // ---- the result, through the stages (no MMA reads them any more)
+      // (this tile's last product first: the other tile's is then at most one
+      // phase behind the one waited for)
+      if (nt > 0) att_tc_wait(&bars[C::B_PV + X], (nt - 1) & 1, ok, err, lane);
+      if (nt > 0 && X + 1 < nx) att_tc_wait(&bars[C::B_PV + 1], (nt - 1) & 1, ok, err, lane);
+      att_tc_fence_after();
+      float* row = reinterpret_cast<float*>(io + lane * C::IO_ROW);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (nt > 0 && ok) {
+          att_tc_ld32(to + 32 * c, o);
+          att_tc_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<uint4*>(row + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      }
+      __syncwarp();
+      constexpr int V = D / 32;
+      for (int i = 0; i < 32 && wrow + i < nr; ++i) {
+        const float li = __shfl_sync(0xffffffffu, l, i), mi = __shfl_sync(0xffffffffu, m, i);
+        const float* src = reinterpret_cast<const float*>(io + i * C::IO_ROW) + lane * V;
+        float y[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) y[k] = src[k];
+        if (parts > 1) {
+          float* ps = reinterpret_cast<float*>(a.ws + w.partials_off) +
+                      ((int64_t)blockIdx.x * seqs.slot_rows + wrow + i) * (D + 4);
+#pragma unroll
+          for (int k = 0; k < V; ++k) ps[lane * V + k] = y[k];
+          if (lane == 0) {
+            ps[D] = mi;
+            ps[D + 1] = li;
+          }
+        } else {
+          attend_store_row<D>(g, a, seqs, sq, h, r0 + wrow + i, y, li, lane);
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ================= operands: 16 of the tile's 64 tokens per warp =================
+    const int c2 = (warp - 8) >> 1, sub = (warp - 8) & 1, te = 4 * c2 + 2 * sub;
+    const unsigned char* blocks =
+        a.cache + g.blocks_off + ((int64_t)seq * g.hkv + h) * g.max_groups * g.block_bytes;
+    const __half* sink = reinterpret_cast<const __half*>(a.cache + g.sinks_off + ((int64_t)seq * g.hkv + h) * g.sink_bytes);
+    const __half* tail = reinterpret_cast<const __half*>(a.cache + g.tails_off + ((int64_t)seq * g.hkv + h) * g.tail_bytes);
+    for (int t = 0; t < nt && ok; ++t) {
+      const int st = t % C::NST, c = 2 * (t0 + t) + c2;
+      unsigned char* stage = smem + st * C::STAGE;
+      auto wait = [&] {
+        if (t >= C::NST) att_tc_wait(&bars[C::B_EMPTY + st], (t / C::NST - 1) & 1, ok, err, lane);
+      };
+      if (c < keys.nblk * keys.per) {
+        const int grp = keys.group(c);
+        const unsigned char* blk = blocks + (int64_t)grp * g.block_bytes;
+        bool narrow = false;
+        if constexpr (KB == 4) {
+          narrow = g.akvq_delta && akvq_key_bits(grp, n, G, g.akvq_delta) == 2;
+          if (narrow) tc_fill_block<D, 2, VB, G>(blk, c % keys.per, sub, stage, te, lane, wait);
+        }
+        if (!narrow) tc_fill_block<D, KB, VB, G>(blk, c % keys.per, sub, stage, te, lane, wait);
+      } else {
+        int pos, valid;
+        keys.at(c, &pos, &valid);
+        const bool in_sink = c < keys.nblk * keys.per + keys.nsink;
+        valid = min(16, valid - 16 * sub);
+        const int slot = in_sink ? pos + 16 * sub : (pos + 16 * sub - keys.S) % g.tail_slots;
+        const __half* k = (in_sink ? sink : tail) + slot * D;
+        tc_fill_fp16<D>(k, k + (in_sink ? g.sink_slots : g.tail_slots) * D, valid, stage, te, lane, wait);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[C::B_FULL + st]);
+    }
+  } else {
+    // ================= MMA issue: one elected lane =================
+    constexpr uint32_t ID_QK = att_tc_idesc(kTcKeys), ID_PV = att_tc_idesc(D);
+    const uint32_t sb = smem_u32(smem);
+    auto qk = [&](int t, int x) {
+      const uint32_t base = sb + (t % C::NST) * C::STAGE;
+      const uint64_t d1 = att_tc_desc(base, D * 16), d2 = att_tc_desc(base + C::K_BYTES, D * 16);
+      const uint32_t d = tm + C::T_S + kTcKeys * x, q = tm + C::T_Q + (D / 2) * x;
+      att_tc_fence_after();
+      if (ok && att_elect()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) att_tc_mma(d, q + 8 * k, d1 + 16 * k, ID_QK, k > 0);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) att_tc_mma(d, q + 8 * k, d2 + 16 * k, ID_QK, 1u);
+        if (exact) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) att_tc_mma(d, q + D / 2 + 8 * k, d1 + 16 * k, ID_QK, 1u);
+        }
+        att_tc_commit(&bars[C::B_S + x]);
+      }
+      __syncwarp();
+    };
+    if (nt > 0) {
+      att_tc_wait(&bars[C::B_FULL], 0, ok, err, lane);
+      for (int x = 0; x < nx; ++x) qk(0, x);
+    }
+    for (int t = 0; t < nt; ++t) {
+      for (int x = 0; x < nx; ++x) {
+        att_tc_wait(&bars[C::B_P + x], t & 1, ok, err, lane);
+        att_tc_fence_after();
+        const uint64_t dv = att_tc_desc(sb + (t % C::NST) * C::STAGE + 2 * C::K_BYTES, kTcKeys * 16);
+        const uint32_t d = tm + C::T_O + D * x, p = tm + C::T_S + kTcKeys * x;
+        if (ok && att_elect()) {
+#pragma unroll
+          for (int k = 0; k < kTcKeys / 16; ++k)
+            att_tc_mma(d, p + 8 * k, dv + 16 * k, ID_PV, t > 0 || k > 0);
+          att_tc_commit(&bars[C::B_PV + x]);
+          if (x == nx - 1) att_tc_commit(&bars[C::B_EMPTY + t % C::NST]);
+        }
+        __syncwarp();
+        if (t + 1 < nt) {
+          if (x == 0) att_tc_wait(&bars[C::B_FULL + (t + 1) % C::NST], ((t + 1) / C::NST) & 1, ok, err, lane);
+          // the next S goes over P, which this product has to have read
+          att_tc_wait(&bars[C::B_PV + x], t & 1, ok, err, lane);
+          qk(t + 1, x);
+        }
+      }
+    }
+  }
+  att_tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    att_tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(C::T_COLS)
+                 : "memory");
+  }
+}
+
+template <int D, int KB, int VB, int G>
+cudaError_t launch_attend_tc_t(const Geom& g, const WsLayout& w, const AttendArgs& a,
+                               const AttendSeqs& s, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, KB, VB, G>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, TcAtt<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  attend_tc_kernel<D, KB, VB, G>
+      <<<(unsigned)s.piece_off[s.n], kTcThreads, TcAtt<D>::SMEM, stream>>>(g, w, a, s);
+  return cudaGetLastError();
+}
+
+template <int D, int KB, int VB, int G>
+cudaError_t launch_attend_t(const Geom& g, const WsLayout& w, const AttendArgs& a,
+                            const AttendSeqs& s, cudaStream_t stream) {
+  using C = AttCfg<D, KB, VB, G>;
+  if (g.block_bytes != C::BLK) return cudaErrorInvalidValue;
+  if (s.unit_rows != kAttendRows) return launch_attend_tc_t<D, KB, VB, G>(g, w, a, s, stream);
+  cudaError_t e = attend_configure<D, KB, VB, G>();
+  if (e != cudaSuccess) return e;
+  attend_kernel<D, KB, VB, G><<<(unsigned)s.piece_off[s.n], kAttThreads, C::SMEM, stream>>>(g, w, a, s);
+  return cudaGetLastError();
+}
+
+#define KVQ_ATTEND_DEFINE(D_, KB_, VB_, G_)                                                       \
+  cudaError_t attend_max_ctas_##D_##_##KB_##_##VB_##_##G_(int* out) {                             \
+    return attend_occupancy<D_, KB_, VB_, G_>(out);                                               \
+  }                                                                                               \
+  cudaError_t launch_attend_##D_##_##KB_##_##VB_##_##G_(const Geom& g, const WsLayout& w,         \
+                                                        const AttendArgs& a, const AttendSeqs& s, \
+                                                        cudaStream_t stream) {                    \
+    return launch_attend_t<D_, KB_, VB_, G_>(g, w, a, s, stream);                                 \
+  }
+
+}  // namespace kvq

@@ -168,6 +168,10 @@ inline void make_ws_layout(const Geom& g, WsLayout* w) {
   w->total = align_up(w->partials_off + 2LL * kMaxDecodeCtas * w->slot_floats * 4, 256);
 }
 
+// The workspace of a cache: kvq_attend's partials start where the decode's do
+// and may be longer.
+inline void make_cache_ws_layout(const Geom& g, WsLayout* w);
+
 // ---- append / quantize ----------------------------------------------------
 // Per-sequence arguments of one append launch.  The current lengths are
 // not among them: the kernel reads them from the device copy, so a captured
@@ -234,9 +238,17 @@ constexpr int kAttendMaxSeqs = 512;
 // Rows (query token, query head) of one unit: the N = 8 columns of the
 // P.V tile.
 constexpr int kAttendRows = 8;
-// Split pieces of one launch that write partials: their slots (kAttendRows
-// rows each) fill the decode workspace's partial region.
-constexpr int kAttendPieces = 2 * kMaxDecodeCtas;
+// Rows (D + 4 floats each) that the partials of one launch's split units may
+// take in a cache's workspace: 148 tensor-core units of 256 rows.
+constexpr int kAttendPartialRows = 148 * 256;
+// From this many rows per kv head on a sequence goes to the tensor-core kernel.
+constexpr int kAttendTcRows = 64;
+
+inline void make_cache_ws_layout(const Geom& g, WsLayout* w) {
+  make_ws_layout(g, w);
+  const int64_t end = align_up(w->partials_off + 4LL * kAttendPartialRows * (g.d + 4), 256);
+  if (end > w->total) w->total = end;
+}
 
 struct AttendArgs {
   const unsigned char* cache;
@@ -248,6 +260,7 @@ struct AttendArgs {
   int32_t score_window;      // 0: none
   const float* slopes;       // [hq] or NULL
   const int32_t* prefix;     // [n_seq] or NULL
+  int32_t residual;          // queries that fp16 does not hold exactly
 };
 
 // Sequence i of a launch is the cache's seq0 + i; its query rows start at
@@ -255,6 +268,8 @@ struct AttendArgs {
 // row tile) the same number of pieces, tile after tile.
 struct AttendSeqs {
   int32_t n, seq0;
+  int32_t unit_rows;         // kAttendRows, or 256 / 128 (tensor cores)
+  int32_t slot_rows;         // rows of a piece's partial slot
   int32_t row_off[kAttendMaxSeqs];
   int32_t n_q[kAttendMaxSeqs];
   int32_t piece_off[kAttendMaxSeqs + 1];

@@ -56,17 +56,13 @@ cudaError_t launch_reorder(const Geom&, unsigned char*, const ReorderMoves& m, i
   for (int i = 0; i < n; ++i) put({m.src[i], m.dst[i], m.src_was[i], m.dst_was[i], m.batch[i], m.last[i]});
   return cudaSuccess;
 }
-#include "attend_stub.inc"
-}  // namespace kvq
-"""
-
-ATTEND = r"""
 cudaError_t attend_max_ctas(const Geom&, int* m) { *m = 592; return cudaSuccess; }
-cudaError_t launch_attend(const Geom&, const WsLayout& w, const AttendArgs&, const AttendSeqs& s, bool split, cudaStream_t) {
-  put({1, s.n, s.seq0, split ? 1 : 0, s.piece_off[s.n]});
+cudaError_t launch_attend(const Geom&, const WsLayout& w, const AttendArgs& a, const AttendSeqs& s, bool split, cudaStream_t) {
+  put({1, s.n, s.seq0, split ? 1 : 0, s.piece_off[s.n], s.unit_rows, s.slot_rows, a.residual});
   for (int i = 0; i < s.n; ++i) put({s.row_off[i], s.n_q[i], s.piece_off[i]});
   return cudaSuccess;
 }
+}  // namespace kvq
 """
 
 
@@ -82,11 +78,10 @@ def host_library(folder) -> ctypes.CDLL:
     if not gxx or not inc:
         pytest.skip("g++ or the CUDA headers are not available")
     (folder / "stub.cpp").write_text(STUB)
-    (folder / "attend_stub.inc").write_text(ATTEND)
     csrc = os.path.join(ROOT, "asymmetric_kv_cache_b200", "csrc")
     lib = folder / "libkvq_host.so"
-    cmd = [gxx, "-std=c++17", "-O1", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-I", inc, "-I", csrc, "-I", os.path.join(ROOT, "include"), "-I",
-           str(folder), os.path.join(csrc, "kvq_abi.cpp"), str(folder / "stub.cpp"), "-o", str(lib)]
+    cmd = [gxx, "-std=c++17", "-O1", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-I", inc, "-I", csrc, "-I", os.path.join(ROOT, "include"),
+           os.path.join(csrc, "kvq_abi.cpp"), str(folder / "stub.cpp"), "-o", str(lib)]
     res = subprocess.run(cmd, capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
     return ctypes.CDLL(str(lib))

@@ -51,36 +51,44 @@ def test_attend_refusals(host):
     assert _attend(host, h, n_q=[100, 1, 0, 300]) == 0 and host.log()
 
 
-@pytest.mark.parametrize("seed", range(6))
-def test_attend_plan(host, seed):
-    """Rows and pieces of every launch: all rows covered in order, every unit of a sequence in the same number of pieces, no
-    more pieces than the partials' slots where units are cut."""
+@pytest.mark.parametrize("dt", [0, 2])
+@pytest.mark.parametrize("seed", range(8))
+def test_attend_plan(host, seed, dt):
+    """Rows and pieces of every launch: every sequence in exactly one kernel's launch, rows in the call's order, every unit of a
+    sequence in the same number of pieces, and no more partial rows than the workspace has where units are cut."""
     r = random.Random(seed)
     seqs = r.choice([1, 3, 8, 70, 700])
     hkv = r.choice([1, 2, 8])
     gqa = r.choice([1, 3, 4, 8])
     lens = [r.choice([1, 40, 1000, 4000]) for _ in range(seqs)]
-    n_q = [r.choice([0, 1, 1, min(n, r.randint(1, 50)), n if n < 50 else 7]) for n in lens]
+    n_q = [r.choice([0, 1, 1, min(n, r.randint(1, 50)), n if n < 50 else 7, n]) for n in lens]
     h = host.cache(lens, max_seqs=seqs, n_kv_heads=hkv, n_q_heads=hkv * gqa)
     host.log()
-    assert _attend(host, h, n_q=n_q, window=r.choice([0, 64])) == 0
-    log, row, b = host.log(), 0, 0
+    assert _attend(host, h, n_q=n_q, window=r.choice([0, 64]), dt=dt) == 0
+    first = [sum(n_q[:b]) for b in range(seqs)]
+    log, seen = host.log(), {}
     while log:
-        kind, n, seq0, split, pieces = log[:5]
-        assert kind == 1 and seq0 == b
-        body, log = log[5:5 + 3 * n], log[5 + 3 * n:]
+        kind, n, seq0, split, pieces, unit, slot, residual = log[:8]
+        assert kind == 1 and residual == (dt == 2) and unit in ((8, 128) if residual else (8, 256))
+        body, log = log[8:8 + 3 * n], log[8 + 3 * n:]
         offs = body[2::3] + [pieces]
+        cut = False
         for i in range(n):
-            assert body[3 * i] == row and body[3 * i + 1] == n_q[b]
-            units = hkv * -(-n_q[b] * gqa // 8)
-            got = offs[i + 1] - offs[i]
-            assert got == 0 if units == 0 else got % units == 0 and got >= units
-            if units and got > units:
-                assert split and got // units <= (lens[b] // 32 + 4) // 4
-            row += n_q[b]
-            b += 1
-        assert not split or pieces <= 2048
-    assert row == sum(n_q)
+            b = seq0 + i
+            assert body[3 * i:3 * i + 2] == [first[b], n_q[b]]
+            rows, got = n_q[b] * gqa, offs[i + 1] - offs[i]
+            if got == 0:
+                continue
+            assert b not in seen and (unit > 8) == (rows >= 64)
+            seen[b] = True
+            units = hkv * -(-rows // unit)
+            assert got % units == 0 and got >= units
+            if got > units:
+                cut = True
+                assert got // units <= (lens[b] // (64 if unit > 8 else 32) + 4) // 4 and slot >= min(rows, unit)
+        assert cut == bool(split)
+        assert not split or pieces * slot * (128 + 4) * 4 <= host.ws - 512
+    assert sorted(seen) == [b for b in range(seqs) if n_q[b]]
 
 
 # ---------------------------------------------------------------- norm_rotary

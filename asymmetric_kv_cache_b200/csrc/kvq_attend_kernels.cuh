@@ -58,22 +58,86 @@ struct AttCfg {
 // What a row's scores need (row g8 of the tile, the same in its four lanes).
 struct RowRule {
   int pos, prefix, window;   // window: INT_MAX when there is none
-  float scale2, cap2, inv_cap2, slope2;   // times log2(e) where they end in an exponent
+  float scale2;              // scale * log2(e): dot products to exponents of 2
+  float cap2, inv_cap;       // cap * log2(e) and scale / cap; 0 when there is none
+  float slope2;              // slope * log2(e)
 };
+__device__ __forceinline__ RowRule att_rule(const AttendArgs& a, int pos, int prefix, int window,
+                                            int head) {
+  RowRule rr;
+  rr.pos = pos;
+  rr.prefix = prefix;
+  rr.window = window;
+  rr.scale2 = a.scale * kLog2e;
+  rr.cap2 = a.cap * kLog2e;
+  rr.inv_cap = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  rr.slope2 = a.slopes ? a.slopes[head] * kLog2e : 0.f;
+  return rr;
+}
 
-// The score of key j in the exp2 domain.  tanh(x) = 1 - 2 / (1 + e^(2x)): its
-// error of a few 2^-24 is absolute, and the cap multiplies it, 3e-6 at 50.
-__device__ __forceinline__ float att_score(const RowRule& rr, float dot, int j) {
-  float s;
-  if (rr.cap2 != 0.f) {
-    const float e = fast_exp2(dot * rr.inv_cap2);
-    s = rr.cap2 - __fdividef(2.f * rr.cap2, 1.f + e);
-    s = e > 1e37f ? rr.cap2 : s;
-  } else {
-    s = dot * rr.scale2;
+// Two fp32 numbers in a register pair: sm_100's packed arithmetic does two
+// lanes' worth of work per issued instruction.
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void upk2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// x (dot products) -> cap tanh(scale x / cap), in exponents of 2, for the N
+// scores of a lane; the warp's lanes call it together.  Where every argument
+// t of the warp is within 3/4, tanh(t) = t p(t^2) with p the polynomial that
+// agrees with tanh(sqrt z) / sqrt z at the six Chebyshev points of [0, 9/16]
+// (off by 9.4e-8 at most in fp32: 5e-6 in a score capped at 50); elsewhere
+// 1 - 2 / (1 + e^(2t)), off by a few 2^-24.  The polynomial is 4 issue slots
+// a score in packed form, the other two special-function results, of which
+// an SM gives 16 a cycle.
+template <int N>
+__device__ __forceinline__ void att_cap(const RowRule& rr, float (&x)[N]) {
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(x[i]));
+  if (__any_sync(0xffffffffu, !(big * rr.inv_cap <= 0.75f))) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = fast_exp2(x[i] * rr.inv_cap * (2.f * kLog2e));
+      // e may be infinite: 2 / inf = 0; past 2^126 the approximate division gives 0 too
+      x[i] = rr.cap2 - __fdividef(2.f * rr.cap2, 1.f + e);
+    }
+    return;
   }
-  const int far = rr.pos - j;
-  return s - rr.slope2 * (float)(far < 0 ? -far : far);
+  constexpr float kP[6] = {1.0f, -0.33332953f, 0.1332534f, -0.053341117f, 0.019576216f, -0.0047115223f};
+  const uint64_t inv = pk2(rr.inv_cap, rr.inv_cap);
+  uint64_t c[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) c[i] = pk2(kP[i] * rr.cap2, kP[i] * rr.cap2);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const uint64_t t = mul2(pk2(x[i], x[i + 1]), inv), z = mul2(t, t);
+    uint64_t r = fma2(c[5], z, c[4]);
+    r = fma2(r, z, c[3]);
+    r = fma2(r, z, c[2]);
+    r = fma2(r, z, c[1]);
+    r = fma2(r, z, c[0]);
+    upk2(mul2(r, t), x[i], x[i + 1]);
+  }
 }
 __device__ __forceinline__ bool att_visible(const RowRule& rr, int j) {
   return (j <= rr.pos && rr.pos - j < rr.window) || j < rr.prefix;
@@ -131,16 +195,29 @@ __device__ __forceinline__ void att_softmax(AttState<MT>& st, float (&s)[NT][2],
 template <int NT>
 __device__ __forceinline__ void att_scores(const RowRule& rr, const float (&c)[NT][4], float bias,
                                            int pos0, bool masked, int lane, float (&s)[NT][2]) {
-  const int i4 = lane & 3;
+  const int j0 = pos0 + 2 * (lane & 3);
+  float x[2 * NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int i = 0; i < 2 * NT; ++i) x[i] = c[i / 2][i & 1] + c[i / 2][(i & 1) + 2] + bias;
+  if (rr.cap2 != 0.f) {
+    att_cap(rr, x);
+  } else {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int j = pos0 + 8 * nt + 2 * i4 + e;
-      const float x = att_score(rr, c[nt][e] + c[nt][e + 2] + bias, j);
-      s[nt][e] = !masked || att_visible(rr, j) ? x : -INFINITY;
-    }
+    for (int i = 0; i < 2 * NT; ++i) x[i] *= rr.scale2;
   }
+  if (rr.slope2 != 0.f) {
+    const float far = (float)(rr.pos - j0);
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i)
+      x[i] = fmaf(-rr.slope2, fabsf(far - (float)(8 * (i / 2) + (i & 1))), x[i]);
+  }
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i)
+      if (!att_visible(rr, j0 + 8 * (i / 2) + (i & 1))) x[i] = -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i) s[i / 2][i & 1] = x[i];
 }
 
 // 32 tokens (half hf of a 64-token block) of a block in shared memory, with
@@ -386,18 +463,8 @@ __global__ void __launch_bounds__(kAttThreads, 4)
   }
   __syncthreads();
 
-  RowRule rr;
-  {
-    const int r = dup ? g8 & 3 : g8;
-    const int rc = min(r, nr - 1);
-    rr.pos = n - nq + (r0 + rc) / g.gqa;
-    rr.prefix = prefix;
-    rr.window = window;
-    rr.scale2 = a.scale * kLog2e;
-    rr.cap2 = a.cap * kLog2e;
-    rr.inv_cap2 = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
-    rr.slope2 = a.slopes ? a.slopes[h * g.gqa + (r0 + rc) % g.gqa] * kLog2e : 0.f;
-  }
+  const int rc = min(dup ? g8 & 3 : g8, nr - 1);
+  const RowRule rr = att_rule(a, n - nq + (r0 + rc) / g.gqa, prefix, window, h * g.gqa + (r0 + rc) % g.gqa);
   AttState<C::MT> st;
 #pragma unroll
   for (int mt = 0; mt < C::MT; ++mt) st.o[mt][0] = st.o[mt][1] = st.o[mt][2] = st.o[mt][3] = 0.f;

@@ -152,6 +152,11 @@ __device__ __forceinline__ uint32_t hsub2_b(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The lowest min(max(n, 0), 32) bits.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 template <int N>
 __device__ __forceinline__ void ldg_words(const void* p, uint32_t (&w)[N]) {
   if constexpr (N % 4 == 0) {
@@ -412,18 +417,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (X < nx) {
       // ================= softmax: a thread per row =================
       const int r = wrow + lane, rc = min(r, nr - 1);
-      RowRule rr;
-      rr.pos = n - nq + (r0 + rc) / g.gqa;
-      rr.prefix = prefix;
-      rr.window = window;
-      rr.scale2 = a.scale * kLog2e;
-      rr.cap2 = a.cap * kLog2e;
-      rr.inv_cap2 = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
-      rr.slope2 = a.slopes ? a.slopes[h * g.gqa + (r0 + rc) % g.gqa] * kLog2e : 0.f;
+      const RowRule rr = att_rule(a, n - nq + (r0 + rc) / g.gqa, prefix, window, h * g.gqa + (r0 + rc) % g.gqa);
       // positions of this warp's rows
       const int w_lo = n - nq + (r0 + min(wrow, nr - 1)) / g.gqa;
       const int w_hi = n - nq + (r0 + min(wrow + 31, nr - 1)) / g.gqa;
-      const bool plain = a.cap == 0.f && !a.slopes;
       float m = -INFINITY, l = 0.f;
       const uint32_t ts = tm + lanes + C::T_S + kTcKeys * X, to = tm + lanes + C::T_O + D * X;
       for (int t = 0; t < nt; ++t) {
@@ -434,32 +431,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         att_tc_ld32(ts, reinterpret_cast<uint32_t*>(s));
         att_tc_ld32(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
         att_tc_wait_ld();
+        // exponents are s mul (dot products keep their scale for the one
+        // multiply-add before the exponential)
         float mul = rr.scale2;
-        bool easy = plain;
+        if (a.cap != 0.f) {
+          att_cap(rr, s);
+          mul = 1.f;
+        } else if (a.slopes) {
+#pragma unroll
+          for (int i = 0; i < kTcKeys; ++i) s[i] *= rr.scale2;
+          mul = 1.f;
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           int pos, valid;
           keys.at(2 * (t0 + t) + c, &pos, &valid);
-          const bool every = valid == 32 && (pos + 32 <= prefix || (pos + 31 <= w_lo && w_hi - pos < window));
-          easy = easy && every;
-        }
-        if (!easy) {
-          mul = 1.f;
+          if (a.slopes) {
+            const float far = (float)(rr.pos - pos);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            int pos, valid;
-            keys.at(2 * (t0 + t) + c, &pos, &valid);
+            for (int i = 0; i < 32; ++i)
+              s[32 * c + i] = fmaf(-rr.slope2, fabsf(far - (float)i), s[32 * c + i]);
+          }
+          if (!(valid == 32 && (pos + 32 <= prefix || (pos + 31 <= w_lo && w_hi - pos < window)))) {
+            // bit i: key pos + i is seen
+            const uint32_t there = low_bits(valid), seen =
+                (low_bits(rr.pos - pos + 1) & ~(rr.pos >= window ? low_bits(rr.pos - window + 1 - pos) : 0u)) |
+                low_bits(prefix - pos);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float x = att_score(rr, s[32 * c + i], pos + i);
-              s[32 * c + i] = i < valid && att_visible(rr, pos + i) ? x : -INFINITY;
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!(there & seen & (1u << i))) s[32 * c + i] = -INFINITY;
           }
         }
-        float mx = s[0];
+        float mxs[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 1; i < kTcKeys; ++i) mx = fmaxf(mx, s[i]);
-        mx *= mul;
+        for (int i = 4; i < kTcKeys; ++i) mxs[i & 3] = fmaxf(mxs[i & 3], s[i]);
+        const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * mul;
         if (__any_sync(0xffffffffu, mx > m + kTcSlack)) {
           const float mn = fmaxf(m, mx);
           const float alpha = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
@@ -482,11 +488,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         const float base = m == -INFINITY ? 0.f : m;
         uint32_t p[kTcKeys / 2];
+        const uint64_t mul_2 = pk2(mul, mul), base_2 = pk2(-base, -base);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int i = 0; i < kTcKeys; i += 2) {
-          const float p0 = fast_exp2(fmaf(s[i], mul, -base)), p1 = fast_exp2(fmaf(s[i + 1], mul, -base));
-          l += p0 + p1;
+          float p0, p1;
+          upk2(fma2(pk2(s[i], s[i + 1]), mul_2, base_2), p0, p1);
+          p0 = fast_exp2(p0);
+          p1 = fast_exp2(p1);
+          sum[i / 2 & 1] = add2(sum[i / 2 & 1], pk2(p0, p1));
           p[i / 2] = pack_h2(p0, p1);
+        }
+        {
+          float x, y;
+          upk2(add2(sum[0], sum[1]), x, y);
+          l += x + y;
         }
         att_tc_st32(ts, p);
         att_tc_wait_st();

@@ -28,6 +28,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 
@@ -101,42 +103,81 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// Largest and smallest of three (one instruction each on sm_100).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The largest of N (N a multiple of 4), by two chains.
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
+#pragma unroll
+  for (int i = 4; i < N; i += 4) {
+    a = max3(a, x[i], x[i + 1]);
+    b = max3(b, x[i + 2], x[i + 3]);
+  }
+  return fmaxf(a, b);
+}
+template <int N>
+__device__ __forceinline__ float min_of(const float (&x)[N]) {
+  float a = fminf(x[0], x[1]), b = fminf(x[2], x[3]);
+#pragma unroll
+  for (int i = 4; i < N; i += 4) {
+    a = min3(a, x[i], x[i + 1]);
+    b = min3(b, x[i + 2], x[i + 3]);
+  }
+  return fminf(a, b);
+}
+
+// cap2 tanh(inv_cap x) by tanh(t) = t p(t^2), p of C coefficients.
+template <int C, int N>
+__device__ __forceinline__ void att_cap_poly(const RowRule& rr, const float (&coef)[C], float (&x)[N]) {
+  const uint64_t inv = pk2(rr.inv_cap, rr.inv_cap);
+  uint64_t c[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) c[i] = pk2(coef[i] * rr.cap2, coef[i] * rr.cap2);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const uint64_t t = mul2(pk2(x[i], x[i + 1]), inv), z = mul2(t, t);
+    uint64_t r = fma2(c[C - 1], z, c[C - 2]);
+#pragma unroll
+    for (int k = C - 3; k >= 0; --k) r = fma2(r, z, c[k]);
+    upk2(mul2(r, t), x[i], x[i + 1]);
+  }
+}
+
 // x (dot products) -> cap tanh(scale x / cap), in exponents of 2, for the N
-// scores of a lane; the warp's lanes call it together.  Where every argument
-// t of the warp is within 3/4, tanh(t) = t p(t^2) with p the polynomial that
-// agrees with tanh(sqrt z) / sqrt z at the six Chebyshev points of [0, 9/16]
-// (off by 9.4e-8 at most in fp32: 5e-6 in a score capped at 50); elsewhere
-// 1 - 2 / (1 + e^(2t)), off by a few 2^-24.  The polynomial is 4 issue slots
-// a score in packed form, the other two special-function results, of which
-// an SM gives 16 a cycle.
+// scores of a lane; the warp's lanes call it together.  With every argument t
+// of the warp within T, tanh(t) = t p(t^2), p the polynomial that agrees with
+// tanh(sqrt z) / sqrt z at the Chebyshev points of [0, T^2]: four
+// coefficients for T = 1/2 (off by 2.6e-7 in fp32: 1.3e-5 in a score capped at
+// 50, a twentieth of the weight's rounding to fp16), seven for T = 1 (1.0e-7).
+// Elsewhere 1 - 2 / (1 + e^(2t)), off by a few 2^-24, which takes two special
+// function results a score, of which an SM gives 16 a cycle: the 7268 us of
+// that form alone for 2048 tokens over two contexts of 18k became 2829.
 template <int N>
 __device__ __forceinline__ void att_cap(const RowRule& rr, float (&x)[N]) {
-  float big = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(x[i]));
-  if (__any_sync(0xffffffffu, !(big * rr.inv_cap <= 0.75f))) {
+  constexpr float kP4[4] = {0.999999464f, -0.333262831f, 0.131899402f, -0.0443927385f};
+  constexpr float kP7[7] = {0.99999994f, -0.333328277f, 0.133250758f, -0.0534516461f, 0.0202797074f, -0.0061943247f, 0.00103802513f};
+  const float big = fmaxf(max_of(x), -min_of(x)) * rr.inv_cap;
+  if (__all_sync(0xffffffffu, big <= 0.5f)) {
+    att_cap_poly(rr, kP4, x);
+  } else if (__all_sync(0xffffffffu, big <= 1.0f)) {
+    att_cap_poly(rr, kP7, x);
+  } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float e = fast_exp2(x[i] * rr.inv_cap * (2.f * kLog2e));
       // e may be infinite: 2 / inf = 0; past 2^126 the approximate division gives 0 too
       x[i] = rr.cap2 - __fdividef(2.f * rr.cap2, 1.f + e);
     }
-    return;
-  }
-  constexpr float kP[6] = {1.0f, -0.33332953f, 0.1332534f, -0.053341117f, 0.019576216f, -0.0047115223f};
-  const uint64_t inv = pk2(rr.inv_cap, rr.inv_cap);
-  uint64_t c[6];
-#pragma unroll
-  for (int i = 0; i < 6; ++i) c[i] = pk2(kP[i] * rr.cap2, kP[i] * rr.cap2);
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const uint64_t t = mul2(pk2(x[i], x[i + 1]), inv), z = mul2(t, t);
-    uint64_t r = fma2(c[5], z, c[4]);
-    r = fma2(r, z, c[3]);
-    r = fma2(r, z, c[2]);
-    r = fma2(r, z, c[1]);
-    r = fma2(r, z, c[0]);
-    upk2(mul2(r, t), x[i], x[i + 1]);
   }
 }
 __device__ __forceinline__ bool att_visible(const RowRule& rr, int j) {
@@ -593,11 +634,17 @@ __global__ void __launch_bounds__(kAttThreads, 4)
 }
 
 // The kernel's shared memory is above the default limit for some blocks; the
-// attribute belongs to the device, and setting it again is harmless.
+// attribute belongs to the device and is set once on each.
 template <int D, int KB, int VB, int G>
 cudaError_t attend_configure() {
-  return cudaFuncSetAttribute(attend_kernel<D, KB, VB, G>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, AttCfg<D, KB, VB, G>::SMEM);
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (ready.load() >> (dev & 63) & 1)) return e;
+  e = cudaFuncSetAttribute(attend_kernel<D, KB, VB, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           AttCfg<D, KB, VB, G>::SMEM);
+  if (e == cudaSuccess) ready.fetch_or(1ull << (dev & 63));
+  return e;
 }
 template <int D, int KB, int VB, int G>
 cudaError_t attend_occupancy(int* out) {

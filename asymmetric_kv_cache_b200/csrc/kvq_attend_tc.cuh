@@ -4,16 +4,20 @@
 // kv head's n_q * gqa rows) = two row tiles A and B of M = 128, one CTA per
 // unit (per part of its key list, when there are few units).  Keys come in
 // tiles of 64 tokens that both row tiles use:
-//   * 4 warps turn the codes into operands in shared memory: k = s code + z
+//   * one warp copies the blocks into a ring, bulk copies ahead of their use;
+//   * two groups of 4 warps, a tile each in turn, turn the codes into operands
+//     in shared memory: k = s code + z
 //     as an fp16 value K1 and the fp16 residual K2 of the exact number (the
 //     product's by a fused multiply-subtract, the sum's by the error-free
 //     two-sum), v = s code + z rounded to fp16 once.  The codes' storage
 //     order is the order of the operand's 8 x 16-byte core matrices, a lane's
 //     pair per core row, so every 32-lane store is one core matrix.
-//   * one thread issues S = Q K1^T + Q K2^T (Q as A operand in tensor memory:
-//     from shared memory it would take the bandwidth that K needs, 128 + 64
-//     bytes a cycle of 128) and O += P V (P in tensor memory, over S).
-//   * 4 warps per row tile, a thread per row, turn S into P: no exchange
+//   * S = Q K1^T + Q K2^T (Q as A operand in tensor memory: from shared memory
+//     it would take the bandwidth that K needs, 128 + 64 bytes a cycle of
+//     128) and O += P V (P from shared memory, so that the next S may follow
+//     as soon as this one is in registers) run on the tensor cores while the
+//     softmax of the tile before runs.
+//   * 4 warps per row tile, a thread per row, turn S into P, without exchange
 //     between threads.  The maximum that the weights refer to is only moved
 //     when a score passes it by 2^8, so O in tensor memory is rarely
 //     rescaled; weights stay below 2^8 and the sum is fp32.
@@ -22,30 +26,41 @@
 // the third product Q2 K1^T.
 #pragma once
 
+#include <atomic>
+
 #include "kvq_attend_kernels.cuh"
 
 namespace kvq {
 
 constexpr int kTcRows = 256;              // rows of a unit (kTcRows / 2 with residuals)
 constexpr int kTcKeys = 64;               // keys of a tile
-constexpr int kTcWarps = 13;              // 4 + 4 softmax, 4 operands, 1 issue
+constexpr int kTcWarps = 20;              // 4 + 4 softmax, 4 + 4 operands, 2 issue, copies, 1 idle
 constexpr int kTcThreads = 32 * kTcWarps;
+// Registers a thread: the launch gives kTcRegs to each, which the warp groups
+// (of 128 threads) redistribute: 2 softmax, 2 operand groups, the rest.
+constexpr int kTcRegs = 96, kTcRegsSoftmax = 136, kTcRegsOperands = 88, kTcRegsRest = 32;
+static_assert(2 * kTcRegsSoftmax + 2 * kTcRegsOperands + kTcRegsRest <= 5 * kTcRegs,
+              "the groups' registers come out of the launch's");
 constexpr float kTcSlack = 8.f;           // a maximum may be passed by 2^8 before O is rescaled
 
 template <int D>
 struct TcAtt {
+  // blocks on their way: 64 tokens of the largest blocks (K4 / V4: 40 D bytes a 32)
+  static constexpr int RAW = 80 * D, NRAW = 3;
   static constexpr int K_BYTES = kTcKeys * D * 2;        // K1, K2, V each
   static constexpr int STAGE = 3 * K_BYTES;
-  static constexpr int NST = D == 128 ? 4 : 6;
+  static constexpr int NST = 3;                          // (the barriers of the tiles rely on it)
+  static constexpr int P_BYTES = 128 * kTcKeys * 2;      // of one row tile
   // the query's rows on their way in, and the result's on their way out, use
   // the stages before and after the tiles: per softmax warp 32 padded rows
   static constexpr int IO_ROW = 4 * D + 16;
   static constexpr int IO_BYTES = 8 * 32 * IO_ROW;
   static constexpr int AREA = NST * STAGE > IO_BYTES ? NST * STAGE : IO_BYTES;
-  static constexpr int BAR = AREA;
-  // barriers: full[NST], empty[NST], s_full[2], p_full[2], pv_done[2]
-  static constexpr int B_FULL = 0, B_EMPTY = NST, B_S = 2 * NST, B_P = B_S + 2, B_PV = B_P + 2,
-                       NBAR = B_PV + 2;
+  static constexpr int P_OFF = AREA;
+  static constexpr int RAW_OFF = P_OFF + 2 * P_BYTES;
+  static constexpr int BAR = RAW_OFF + NRAW * RAW;
+  // mbarriers: empty[NST], s_full[2], pv_done[2], raw_full[NRAW], raw_empty[NRAW]
+  static constexpr int B_EMPTY = 0, B_S = NST, B_PV = B_S + 2, B_RF = B_PV + 2, B_RE = B_RF + NRAW, NBAR = B_RE + NRAW;
   static constexpr int SMEM = BAR + NBAR * 8;
   // tensor memory columns
   static constexpr uint32_t T_S = 0, T_Q = 128, T_O = 128 + D, T_COLS = 512;
@@ -62,6 +77,15 @@ __device__ __forceinline__ void att_tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
+}
+// D (tensor memory) (+)= A (shared-memory descriptor) * B (the same)
+__device__ __forceinline__ void att_tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 // D (tensor memory) (+)= A (tensor memory) * B (shared-memory descriptor)
 __device__ __forceinline__ void att_tc_mma(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
@@ -118,24 +142,28 @@ __host__ __device__ constexpr uint32_t att_tc_idesc(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// Bounded wait (2^14 tries that sleep up to 20 us each in hardware); a wait
-// that runs out clears the warp's `ok` and is recorded.
+// Hand-offs.  Warps that wait on an mbarrier read it again and again, and
+// every shared-memory operation of the CTA queues behind those reads (with 18
+// waiting warps a plain load took 102 cycles and a wait on a completed
+// barrier 274).  So of the operand warps, which wait most of the time, one
+// polls for its team and the others wait at a hardware barrier, which costs
+// nothing; and hand-offs to the issuing warp (S read, P written, operands
+// written) are hardware barriers: the giving side arrives, that warp syncs.  Every barrier's next use waits, by
+// the data flow, for the issuing warp to have passed this one.
+// A polled wait is bounded; one that runs out is recorded, later ones of the
+// warp are skipped, and the roles run on to their ends over whatever the
+// buffers hold, so that all meet at every hardware barrier.
+enum { kBarOp0 = 1, kBarOp1, kBarSrA, kBarSrB, kBarPA, kBarPB, kBarFull0, kBarFull1 };
+__device__ __forceinline__ void att_bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void att_bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 __device__ __forceinline__ void att_tc_wait(uint64_t* bar, uint32_t parity, bool& ok, int32_t* err,
                                             int lane) {
   if (!ok) return;
-  bool got = false;
-  for (int it = 0; it < (1 << 14) && !got; ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    got = done != 0;
-  }
-  if (!__all_sync(0xffffffffu, got)) {
+  if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity))) {
     ok = false;
     if (lane == 0) atomicExch(err, KVQ_ERR_DEVICE);
   }
@@ -157,25 +185,8 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-template <int N>
-__device__ __forceinline__ void ldg_words(const void* p, uint32_t (&w)[N]) {
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
-      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
-    }
-  } else if constexpr (N == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = v.x; w[1] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
-  }
-}
-
-// Operands of 16 tokens (16-token part `sub` of the 32 tokens hf of a block):
-// token eights te, te + 1 of the tile.  `wait` is called between the loads
+// Operands of 16 tokens (16-token part `sub` of the 32 tokens hf of a block in
+// shared memory): token eights te, te + 1 of the tile.  `wait` is called between the loads
 // and the stores.
 template <int D, int KBL, int VB, int G, class Wait>
 __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, int sub,
@@ -188,13 +199,14 @@ __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, 
                 OFF_VS = OFF_V + G * D * VB / 8, OFF_VZ = OFF_VS + 2 * G * J;
   const int i4 = lane & 3, kv = 2 * hf + sub;
   uint32_t kw[2][WK], ks[P], kz[P], vw[WV], vs[2 * J], vz[2 * J];
+  auto word = [&](int off) { return reinterpret_cast<const uint32_t*>(blk + off); };
 #pragma unroll
-  for (int x = 0; x < 2; ++x) ldg_words<WK>(blk + ((2 * kv + x) * 32 + lane) * LBK, kw[x]);
-  ldg_words<P>(blk + OFF_S + i4 * (D / 2), ks);
-  ldg_words<P>(blk + OFF_Z + i4 * (D / 2), kz);
-  ldg_words<WV>(blk + OFF_V + (kv * 32 + lane) * (4 * WV), vw);
-  ldg_words<2 * J>(blk + OFF_VS + (4 * kv + i4) * J * 8, vs);
-  ldg_words<2 * J>(blk + OFF_VZ + (4 * kv + i4) * J * 8, vz);
+  for (int x = 0; x < 2; ++x) lds_words<WK>(word(((2 * kv + x) * 32 + lane) * LBK), kw[x]);
+  lds_words<P>(word(OFF_S + i4 * (D / 2)), ks);
+  lds_words<P>(word(OFF_Z + i4 * (D / 2)), kz);
+  lds_words<WV>(word(OFF_V + (kv * 32 + lane) * (4 * WV)), vw);
+  lds_words<2 * J>(word(OFF_VS + (4 * kv + i4) * J * 8), vs);
+  lds_words<2 * J>(word(OFF_VZ + (4 * kv + i4) * J * 8), vz);
   wait();
   unsigned char* k1 = stage + te * P * 128 + lane * 4;
   unsigned char* v1 = stage + 2 * TcAtt<D>::K_BYTES + te * 128 + lane * 4;
@@ -287,7 +299,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   unsigned char* const smem = att_tc_smem;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR);
   __shared__ uint32_t tmem_base;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the shuffles tell the compiler that these are the same in all lanes: the
+  // products' operands then stay in uniform registers)
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int32_t* err = reinterpret_cast<int32_t*>(a.ws + w.err_off);
 
   // ---- this piece
@@ -311,11 +325,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int r0 = tile * unit_rows, nr = min(unit_rows, R - r0);
   const int nx = nr > 128 ? 2 : 1;         // row tiles in use
   const int seq = seqs.seq0 + sq;
-  const int n = min(max(reinterpret_cast<const int32_t*>(a.cache + g.lens_off)[seq], 0), g.max_tokens);
+  const int n = __shfl_sync(0xffffffffu, min(max(reinterpret_cast<const int32_t*>(a.cache + g.lens_off)[seq], 0), g.max_tokens), 0);
 
   const int ng = quantized_groups_s(n, G, g.window, g.sink);
   const int window = a.score_window > 0 ? a.score_window : 0x7fffffff;
-  const int prefix = a.prefix ? min(max(a.prefix[seq], 0), n) : 0;
+  const int prefix = __shfl_sync(0xffffffffu, a.prefix ? min(max(a.prefix[seq], 0), n) : 0, 0);
   const int p_lo = n - nq + r0 / g.gqa, p_hi = n - nq + (r0 + nr - 1) / g.gqa;
   const int first = max(0, p_lo >= window ? p_lo - window + 1 : 0);
   TcKeys keys;
@@ -338,18 +352,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int nt = t1 - t0;
 
   if (tid == 0) {
-    for (int s = 0; s < C::NST; ++s) {
-      mbar_init(&bars[C::B_FULL + s], 4);
-      mbar_init(&bars[C::B_EMPTY + s], 1);
-    }
+    for (int s = 0; s < C::NST; ++s) mbar_init(&bars[C::B_EMPTY + s], nx);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[C::B_S + x], 1);
-      mbar_init(&bars[C::B_P + x], 4);
       mbar_init(&bars[C::B_PV + x], 1);
+    }
+    for (int s = 0; s < C::NRAW; ++s) {
+      mbar_init(&bars[C::B_RF + s], 1);
+      mbar_init(&bars[C::B_RE + s], 4);
     }
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&tmem_base)),
                  "r"(C::T_COLS)
@@ -390,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   att_tc_fence_before();
   __syncthreads();
   att_tc_fence_after();
-  const uint32_t tm = tmem_base;
+  const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
   if (warp < 8 && X < nx) {
     const uint4* src = reinterpret_cast<const uint4*>(io + lane * C::IO_ROW);
@@ -414,6 +428,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   bool ok = true;
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsSoftmax));
     if (X < nx) {
       // ================= softmax: a thread per row =================
       const int r = wrow + lane, rc = min(r, nr - 1);
@@ -421,59 +436,73 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // positions of this warp's rows
       const int w_lo = n - nq + (r0 + min(wrow, nr - 1)) / g.gqa;
       const int w_hi = n - nq + (r0 + min(wrow + 31, nr - 1)) / g.gqa;
+      // key parts (32 tokens) that every row of this warp sees whole: the list's
+      // first c_pre (the prefix) and [c_lo, c_hi) of the blocks from gB on
+      const int nb = keys.nblk * keys.per, c_b = keys.gA * keys.per, pos_b = keys.S + keys.gB * G;
+      const int c_pre = min(nb, max(0, prefix - keys.S) / 32);
+      const int c_lo = c_b + (w_hi >= window && w_hi - window >= pos_b ? (w_hi - window - pos_b) / 32 + 1 : 0);
+      const int c_hi = min(nb, c_b + (w_lo - 31 >= pos_b ? (w_lo - 31 - pos_b) / 32 + 1 : 0));
+      const bool plain = a.cap == 0.f && !a.slopes;
+      // this row of P: core matrices of 8 rows x 8 keys, a row eight 1024 bytes
+      unsigned char* prow = smem + C::P_OFF + X * C::P_BYTES + ((wrow & 127) + lane) / 8 * 1024 + lane % 8 * 16;
       float m = -INFINITY, l = 0.f;
       const uint32_t ts = tm + lanes + C::T_S + kTcKeys * X, to = tm + lanes + C::T_O + D * X;
       for (int t = 0; t < nt; ++t) {
         att_tc_wait(&bars[C::B_S + X], t & 1, ok, err, lane);
-        if (!ok) break;
         att_tc_fence_after();
         float s[kTcKeys];
         att_tc_ld32(ts, reinterpret_cast<uint32_t*>(s));
         att_tc_ld32(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
         att_tc_wait_ld();
+        att_tc_fence_before();
+        if (t + 1 < nt) att_bar_arrive(kBarSrA + X, 160);      // the next S may come
         // exponents are s mul (dot products keep their scale for the one
         // multiply-add before the exponential)
+        const int c0 = 2 * (t0 + t);
+        const bool every = c0 + 2 <= c_pre || (c0 >= c_lo && c0 + 2 <= c_hi);
         float mul = rr.scale2;
-        if (a.cap != 0.f) {
-          att_cap(rr, s);
-          mul = 1.f;
-        } else if (a.slopes) {
+        if (!(plain && every)) {
+          if (a.cap != 0.f) {
+            att_cap(rr, s);
+          } else {
 #pragma unroll
-          for (int i = 0; i < kTcKeys; ++i) s[i] *= rr.scale2;
-          mul = 1.f;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          int pos, valid;
-          keys.at(2 * (t0 + t) + c, &pos, &valid);
-          if (a.slopes) {
-            const float far = (float)(rr.pos - pos);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              s[32 * c + i] = fmaf(-rr.slope2, fabsf(far - (float)i), s[32 * c + i]);
+            for (int i = 0; i < kTcKeys; ++i) s[i] *= rr.scale2;
           }
-          if (!(valid == 32 && (pos + 32 <= prefix || (pos + 31 <= w_lo && w_hi - pos < window)))) {
-            // bit i: key pos + i is seen
-            const uint32_t there = low_bits(valid), seen =
-                (low_bits(rr.pos - pos + 1) & ~(rr.pos >= window ? low_bits(rr.pos - window + 1 - pos) : 0u)) |
-                low_bits(prefix - pos);
+          mul = 1.f;
+          if (!every || a.slopes) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(there & seen & (1u << i))) s[32 * c + i] = -INFINITY;
+            for (int c = 0; c < 2; ++c) {
+              int pos, valid;
+              keys.at(c0 + c, &pos, &valid);
+              if (a.slopes) {
+                const float far = (float)(rr.pos - pos);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  s[32 * c + i] = fmaf(-rr.slope2, fabsf(far - (float)i), s[32 * c + i]);
+              }
+              if (!every) {
+                // bit i: key pos + i is seen
+                const uint32_t seen =
+                    low_bits(valid) &
+                    ((low_bits(rr.pos - pos + 1) &
+                      ~(rr.pos >= window ? low_bits(rr.pos - window + 1 - pos) : 0u)) |
+                     low_bits(prefix - pos));
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(seen & (1u << i))) s[32 * c + i] = -INFINITY;
+              }
+            }
           }
         }
-        float mxs[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int i = 4; i < kTcKeys; ++i) mxs[i & 3] = fmaxf(mxs[i & 3], s[i]);
-        const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * mul;
+        const float mx = max_of(s) * mul;
         if (__any_sync(0xffffffffu, mx > m + kTcSlack)) {
           const float mn = fmaxf(m, mx);
           const float alpha = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
           m = mn;
           l *= alpha;
           if (t > 0) {
+            // O holds the tiles before this one
             att_tc_wait(&bars[C::B_PV + X], (t - 1) & 1, ok, err, lane);
-            if (!ok) break;
             att_tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -484,6 +513,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
               att_tc_st32(to + 32 * c, o);
             }
+            att_tc_wait_st();
+            att_tc_fence_before();
           }
         }
         const float base = m == -INFINITY ? 0.f : m;
@@ -504,23 +535,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           upk2(add2(sum[0], sum[1]), x, y);
           l += x + y;
         }
-        att_tc_st32(ts, p);
-        att_tc_wait_st();
-        att_tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[C::B_P + X]);
+        // the product before this one has read P
+        if (t > 0) att_tc_wait(&bars[C::B_PV + X], (t - 1) & 1, ok, err, lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(prow + 128 * i) =
+              make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+        fence_proxy_async_smem();
+        att_bar_arrive(kBarPA + X, 160);
       }
-      // ---- the result, through the stages (no MMA reads them any more)
-      // (this tile's last product first: the other tile's is then at most one
-      // phase behind the one waited for)
-      if (nt > 0) att_tc_wait(&bars[C::B_PV + X], (nt - 1) & 1, ok, err, lane);
-      if (nt > 0 && X + 1 < nx) att_tc_wait(&bars[C::B_PV + 1], (nt - 1) & 1, ok, err, lane);
+      // ---- the result, through the stages: once both tiles' last products are
+      // done (the last key tile's stage is free: nobody waits for later phases)
+      if (nt > 0) att_tc_wait(&bars[C::B_EMPTY + (nt - 1) % C::NST], (nt - 1) / C::NST & 1, ok, err, lane);
       att_tc_fence_after();
       float* row = reinterpret_cast<float*>(io + lane * C::IO_ROW);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
-        if (nt > 0 && ok) {
+        if (nt > 0) {
           att_tc_ld32(to + 32 * c, o);
           att_tc_wait_ld();
         } else {
@@ -553,22 +585,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-  } else if (warp < 12) {
-    // ================= operands: 16 of the tile's 64 tokens per warp =================
-    const int c2 = (warp - 8) >> 1, sub = (warp - 8) & 1, te = 4 * c2 + 2 * sub;
-    const unsigned char* blocks =
-        a.cache + g.blocks_off + ((int64_t)seq * g.hkv + h) * g.max_groups * g.block_bytes;
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsOperands));
+    // ====== operands: every other tile, 16 of its 64 tokens per warp ======
+    const int c2 = (warp & 3) >> 1, sub = warp & 1, te = 4 * c2 + 2 * sub;
     const __half* sink = reinterpret_cast<const __half*>(a.cache + g.sinks_off + ((int64_t)seq * g.hkv + h) * g.sink_bytes);
     const __half* tail = reinterpret_cast<const __half*>(a.cache + g.tails_off + ((int64_t)seq * g.hkv + h) * g.tail_bytes);
-    for (int t = 0; t < nt && ok; ++t) {
+    const int team = (warp - 8) >> 2;
+    const bool leader = (warp & 3) == 0;
+    for (int t = team; t < nt; t += 2) {
       const int st = t % C::NST, c = 2 * (t0 + t) + c2;
       unsigned char* stage = smem + st * C::STAGE;
       auto wait = [&] {
-        if (t >= C::NST) att_tc_wait(&bars[C::B_EMPTY + st], (t / C::NST - 1) & 1, ok, err, lane);
+        // the stage is free; for the third tile, whose stage is, the first
+        // one's product: the issuing warp has then passed that tile's barrier
+        if (t >= 2) {
+          if (leader && t >= C::NST) att_tc_wait(&bars[C::B_EMPTY + st], (t / C::NST - 1) & 1, ok, err, lane);
+          if (leader && t == 2) att_tc_wait(&bars[C::B_EMPTY], 0, ok, err, lane);
+          att_bar_sync(kBarOp0 + team, 128);
+        }
       };
+      // every warp follows the ring, its own part in a block or not
+      if (leader) att_tc_wait(&bars[C::B_RF + t % C::NRAW], (t / C::NRAW) & 1, ok, err, lane);
+      att_bar_sync(kBarOp0 + team, 128);
       if (c < keys.nblk * keys.per) {
         const int grp = keys.group(c);
-        const unsigned char* blk = blocks + (int64_t)grp * g.block_bytes;
+        const unsigned char* blk = smem + C::RAW_OFF + (t % C::NRAW) * C::RAW + (G == 32 ? c2 * C::RAW / 2 : 0);
         bool narrow = false;
         if constexpr (KB == 4) {
           narrow = g.akvq_delta && akvq_key_bits(grp, n, G, g.akvq_delta) == 2;
@@ -585,61 +627,92 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fill_fp16<D>(k, k + (in_sink ? g.sink_slots : g.tail_slots) * D, valid, stage, te, lane, wait);
       }
       fence_proxy_async_smem();
+      att_bar_arrive(kBarFull0 + team, 128 + 32 * nx);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[C::B_FULL + st]);
+      if (lane == 0) mbar_arrive(&bars[C::B_RE + t % C::NRAW]);
     }
   } else {
-    // ================= MMA issue: one elected lane =================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsRest));
+    if (warp < 16 + nx) {
+    // ====== the products of row tile x: one elected lane ======
+    // (loops, not straight code: the other warps' code leaves little room in
+    // the instruction cache, and a miss costs this warp more than a branch)
     constexpr uint32_t ID_QK = att_tc_idesc(kTcKeys), ID_PV = att_tc_idesc(D);
+    const int x = warp - 16;
     const uint32_t sb = smem_u32(smem);
-    auto qk = [&](int t, int x) {
-      const uint32_t base = sb + (t % C::NST) * C::STAGE;
-      const uint64_t d1 = att_tc_desc(base, D * 16), d2 = att_tc_desc(base + C::K_BYTES, D * 16);
-      const uint32_t d = tm + C::T_S + kTcKeys * x, q = tm + C::T_Q + (D / 2) * x;
-      att_tc_fence_after();
-      if (ok && att_elect()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) att_tc_mma(d, q + 8 * k, d1 + 16 * k, ID_QK, k > 0);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) att_tc_mma(d, q + 8 * k, d2 + 16 * k, ID_QK, 1u);
-        if (exact) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) att_tc_mma(d, q + D / 2 + 8 * k, d1 + 16 * k, ID_QK, 1u);
-        }
-        att_tc_commit(&bars[C::B_S + x]);
-      }
-      __syncwarp();
-    };
-    if (nt > 0) {
-      att_tc_wait(&bars[C::B_FULL], 0, ok, err, lane);
-      for (int x = 0; x < nx; ++x) qk(0, x);
-    }
-    for (int t = 0; t < nt; ++t) {
-      for (int x = 0; x < nx; ++x) {
-        att_tc_wait(&bars[C::B_P + x], t & 1, ok, err, lane);
+    const uint32_t d_s = tm + C::T_S + kTcKeys * x, d_o = tm + C::T_O + D * x, q = tm + C::T_Q + (D / 2) * x;
+    const uint64_t dp = att_tc_desc(sb + C::P_OFF + C::P_BYTES * x, kTcKeys * 16);
+    for (int t = -1; t < nt; ++t) {
+      if (t + 1 < nt) {
+        const uint32_t stage = sb + (t + 1) % C::NST * C::STAGE;
+        const uint64_t d1 = att_tc_desc(stage, D * 16), d2 = att_tc_desc(stage + C::K_BYTES, D * 16);
+        att_bar_sync(kBarFull0 + ((t + 1) & 1), 128 + 32 * nx);
+        // S of the tile before is in the softmax's registers
+        if (t >= 0) att_bar_sync(kBarSrA + x, 160);
         att_tc_fence_after();
-        const uint64_t dv = att_tc_desc(sb + (t % C::NST) * C::STAGE + 2 * C::K_BYTES, kTcKeys * 16);
-        const uint32_t d = tm + C::T_O + D * x, p = tm + C::T_S + kTcKeys * x;
-        if (ok && att_elect()) {
+        if (att_elect()) {
+#pragma unroll 1
+          for (int y = 0; y < (exact ? 3 : 2); ++y) {
+            const uint64_t dk = y == 1 ? d2 : d1;
+            const uint32_t qy = y == 2 ? q + D / 2 : q;
 #pragma unroll
-          for (int k = 0; k < kTcKeys / 16; ++k)
-            att_tc_mma(d, p + 8 * k, dv + 16 * k, ID_PV, t > 0 || k > 0);
-          att_tc_commit(&bars[C::B_PV + x]);
-          if (x == nx - 1) att_tc_commit(&bars[C::B_EMPTY + t % C::NST]);
+            for (int k = 0; k < D / 16; ++k) att_tc_mma(d_s, qy + 8 * k, dk + 16 * k, ID_QK, k > 0 || y > 0);
+          }
+          att_tc_commit(&bars[C::B_S + x]);
         }
         __syncwarp();
-        if (t + 1 < nt) {
-          if (x == 0) att_tc_wait(&bars[C::B_FULL + (t + 1) % C::NST], ((t + 1) / C::NST) & 1, ok, err, lane);
-          // the next S goes over P, which this product has to have read
-          att_tc_wait(&bars[C::B_PV + x], t & 1, ok, err, lane);
-          qk(t + 1, x);
-        }
       }
+      if (t < 0) continue;
+      const uint64_t dv = att_tc_desc(sb + t % C::NST * C::STAGE + 2 * C::K_BYTES, kTcKeys * 16);
+      att_bar_sync(kBarPA + x, 160);
+      att_tc_fence_after();
+      if (att_elect()) {
+#pragma unroll
+        for (int k = 0; k < kTcKeys / 16; ++k)
+          att_tc_mma_ss(d_o, dp + 16 * k, dv + 16 * k, ID_PV, t > 0 || k > 0);
+        att_tc_commit(&bars[C::B_PV + x]);
+        att_tc_commit(&bars[C::B_EMPTY + t % C::NST]);
+      }
+      __syncwarp();
+    }
+    } else if (warp == 18) {
+    // ====== bulk copies of the tiles' blocks ======
+    const unsigned char* blocks =
+        a.cache + g.blocks_off + ((int64_t)seq * g.hkv + h) * g.max_groups * g.block_bytes;
+    for (int t = 0; t < nt; ++t) {
+      const int slot = t % C::NRAW;
+      if (t >= C::NRAW) att_tc_wait(&bars[C::B_RE + slot], (t / C::NRAW - 1) & 1, ok, err, lane);
+      if (lane == 0) {
+        uint32_t bytes[2] = {0u, 0u};
+        int grp[2];
+#pragma unroll
+        for (int i = 0; i < 64 / G; ++i) {
+          const int c = 2 * (t0 + t) + i;
+          if (c >= keys.nblk * keys.per) continue;
+          grp[i] = keys.group(c);
+          bytes[i] = KB == 4 && g.akvq_delta && akvq_key_bits(grp[i], n, G, g.akvq_delta) == 2 ? g.a2_bytes
+                                                                                            : g.block_bytes;
+        }
+        uint64_t* bar = &bars[C::B_RF + slot];
+        if (bytes[0] + bytes[1] > 0) mbar_arrive_expect_tx(bar, bytes[0] + bytes[1]);
+        else mbar_arrive(bar);
+#pragma unroll
+        for (int i = 0; i < 64 / G; ++i)
+          if (bytes[i] > 0)
+            bulk_copy_g2s(smem + C::RAW_OFF + slot * C::RAW + i * (C::RAW / 2),
+                          blocks + (int64_t)grp[i] * g.block_bytes, bytes[i], bar);
+      }
+      __syncwarp();
+    }
+    // copies in flight land before the shared memory goes away (after a
+    // failed wait too)
+    for (int i = max(0, nt - C::NRAW); i < nt; ++i)
+      mbar_wait_bounded(&bars[C::B_RF + i % C::NRAW], (i / C::NRAW) & 1);
     }
   }
   att_tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     att_tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(C::T_COLS)
                  : "memory");
@@ -649,9 +722,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 template <int D, int KB, int VB, int G>
 cudaError_t launch_attend_tc_t(const Geom& g, const WsLayout& w, const AttendArgs& a,
                                const AttendSeqs& s, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, KB, VB, G>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, TcAtt<D>::SMEM);
+  // once per device: the shared memory limit, and that the launch brings the
+  // registers that the warp groups share out (else they would wait for good)
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (!(ready.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(attend_tc_kernel<D, KB, VB, G>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, TcAtt<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, attend_tc_kernel<D, KB, VB, G>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < kTcRegs) return cudaErrorInvalidKernelImage;
+    ready.fetch_or(1ull << (dev & 63));
+  }
   attend_tc_kernel<D, KB, VB, G>
       <<<(unsigned)s.piece_off[s.n], kTcThreads, TcAtt<D>::SMEM, stream>>>(g, w, a, s);
   return cudaGetLastError();

@@ -625,13 +625,13 @@ kvq_status kvq_reorder(kvq_cache* cache, const int32_t* parent, int32_t n_seq,
   for (size_t at = 0; at < all.size();) {
     const size_t from = at;
     at = kvq::next_reorder_launch(all, at, &mv);
-    int64_t bytes = 0;                       // of the longest move of the launch, per kv head
+    int64_t bytes = 0;                       // of the blocks of the longest move, per kv head
     for (size_t i = from; i < at; ++i) {
-      const int n = cache->lens[all[i].src];
-      bytes = std::max(bytes, (int64_t)kvq::quantized_groups_s(n, g.G, g.window, g.sink) * g.block_bytes);
+      const int shared = std::max(0, shared_tokens - g.sink) / g.G;
+      const int groups = kvq::quantized_groups_s(cache->lens[all[i].src], g.G, g.window, g.sink);
+      bytes = std::max(bytes, (int64_t)std::max(0, groups - (g.akvq_delta ? 0 : shared)) * g.block_bytes);
     }
-    const int64_t tiles = ((bytes >> 15) + 2 + (g.sink ? 1 : 0) + (g.tail_bytes >> 15)) * g.hkv;
-    cudaError_t e = kvq::launch_reorder(g, cache->buf, mv, shared_tokens, tiles, (cudaStream_t)stream);
+    cudaError_t e = kvq::launch_reorder(g, cache->buf, mv, shared_tokens, bytes, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "reorder launch");
   }
   std::vector<int32_t> old(cache->lens);

@@ -311,6 +311,6 @@ cudaError_t launch_norm_rotary(int d, int dtype, int out_dtype, const RotaryArgs
 // ---- reordering of sequences ---------------------------------------------
 struct ReorderMoves;         // kvq_reorder_plan.h
 cudaError_t launch_reorder(const Geom& g, unsigned char* cache, const ReorderMoves& mv,
-                           int shared_tokens, int64_t tiles, cudaStream_t stream);
+                           int shared_tokens, int64_t bytes, cudaStream_t stream);
 
 }  // namespace kvq

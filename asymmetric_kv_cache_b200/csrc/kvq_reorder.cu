@@ -16,6 +16,8 @@
 // Lengths: every block reads the device lengths of its chain when it starts
 // and counts itself on the ticket of the chain's first destination; the block
 // that counts last stores the new lengths and puts the ticket back to zero.
+#include <algorithm>
+
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 #include "kvq_reorder_plan.h"
@@ -25,46 +27,65 @@ namespace {
 
 constexpr int kReorderThreads = 256;
 
-// Units [u, u + UN * stride) of one area for a batch of NB moves: read all,
-// write all.  `live(k, unit)` says whether move k carries the unit.
-template <int NB, int UN, class Live>
-__device__ __forceinline__ void move_units(unsigned char* base, const int64_t* so,
-                                           const int64_t* dof, int64_t u, int stride, int64_t end,
-                                           int n, const Live& live) {
+// A batch's move k takes the units [lo, hi) of the area at hand from sequence
+// src to sequence dst.
+struct MoveArea {
+  int32_t src, dst;
+  uint32_t lo, hi;
+};
+
+// The units u, u + kReorderThreads, .. (UN of them) of a batch of n <= NB moves:
+// read all, write all.  `at`: the head's area in sequence 0, `step`: bytes from
+// one sequence's area to the next one's.  AK: the units behind a 2-bit block's
+// end are skipped.
+template <int NB, int UN, bool AK>
+__device__ __forceinline__ void move_units(const Geom& g, unsigned char* at, int64_t step,
+                                           const MoveArea* mv, const int32_t* len, uint32_t u, int n,
+                                           bool blocks, int lo_group) {
   uint4 r[UN][NB];
+  uint32_t live = 0;
 #pragma unroll
-  for (int x = 0; x < UN; ++x)
+  for (int k = 0; k < NB; ++k) {
+    const MoveArea m = mv[k];               // (entries from n on are empty)
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int64_t uu = u + (int64_t)x * stride;
-      if (k < n && uu < end && live(k, uu))
-        r[x][k] = *reinterpret_cast<const uint4*>(base + so[k] + 16 * uu);
+    for (int x = 0; x < UN; ++x) {
+      const uint32_t uu = u + x * kReorderThreads;
+      bool on = uu >= m.lo && uu < m.hi;
+      if (AK && blocks && on) {
+        const uint32_t upb = g.block_bytes / 16;
+        const int grp = lo_group + (int)(uu / upb);
+        on = akvq_key_bits(grp, len[k], g.G, g.akvq_delta) == 4 || (int)(uu % upb) * 16 < g.a2_bytes;
+      }
+      if (on) {
+        live |= 1u << (x * NB + k);
+        r[x][k] = *reinterpret_cast<const uint4*>(at + m.src * step + (int64_t)uu * 16);
+      }
     }
+  }
 #pragma unroll
-  for (int x = 0; x < UN; ++x)
+  for (int k = 0; k < NB; ++k) {
+    const int64_t dst = mv[k].dst * step;
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int64_t uu = u + (int64_t)x * stride;
-      if (k < n && uu < end && live(k, uu))
-        *reinterpret_cast<uint4*>(base + dof[k] + 16 * uu) = r[x][k];
-    }
+    for (int x = 0; x < UN; ++x)
+      if (live & 1u << (x * NB + k))
+        *reinterpret_cast<uint4*>(at + dst + (int64_t)(u + x * kReorderThreads) * 16) = r[x][k];
+  }
 }
 
-// Grid: x = tiles of kReorderThreads * 8 units over (kv head, area), strided;
-// y = chain.
-__global__ void __launch_bounds__(kReorderThreads)
+// Grid: x = tiles of kReorderTile units over (kv head, area), strided; y =
+// chain.  NB: the largest batch of the launch, rounded up to a power of two.  A
+// thread has 8 loads of 16 bytes in flight whatever NB is, 1024 threads on an
+// SM: 128 KB, three times what the memory's latency at its rate needs.
+template <int NB, bool AK>
+__global__ void __launch_bounds__(kReorderThreads, NB == 8 ? 3 : 4)
     reorder_kernel(const Geom g, unsigned char* cache, const ReorderMoves mv, int32_t shared_tokens) {
+  constexpr int kUnits = 8 / NB, kReorderTile = kReorderThreads * kUnits;
   __shared__ int32_t s_len[kReorderMoves], d_len[kReorderMoves];
-  __shared__ int64_t s_off[kReorderBatch], d_off[kReorderBatch];
-  __shared__ int32_t last;
+  __shared__ MoveArea area_of[kReorderBatch];
+  __shared__ int32_t range[2], last;
   const int tid = threadIdx.x;
   const int m0 = mv.chain_start[blockIdx.y], m1 = mv.chain_start[blockIdx.y + 1];
   int32_t* lens = reinterpret_cast<int32_t*>(cache + g.lens_off);
-  for (int m = m0 + tid; m < m1; m += kReorderThreads) {
-    s_len[m - m0] = min(max(lens[mv.src_was[m]], 0), g.max_tokens);
-    d_len[m - m0] = min(max(lens[mv.dst_was[m]], 0), g.max_tokens);
-  }
-  __syncthreads();
   auto groups = [&](int n) { return quantized_groups_s(n, g.G, g.window, g.sink); };
   // groups that stay because source and destination share them: those whose
   // tokens are shared and that are quantized in both.  With position-adaptive
@@ -72,21 +93,30 @@ __global__ void __launch_bounds__(kReorderThreads)
   // bytes: nothing is shared between them then.
   const int shared_groups = shared_tokens > g.sink ? (shared_tokens - g.sink) / g.G : 0;
   auto kept = [&](int sn, int dn) {
-    return g.akvq_delta && sn != dn ? 0 : min(shared_groups, min(groups(sn), groups(dn)));
+    return AK && sn != dn ? 0 : min(shared_groups, min(groups(sn), groups(dn)));
   };
-  int most = 0, lo_group = 0x7fffffff;        // groups of the chain: [lo_group, most)
-  for (int m = 0; m < m1 - m0; ++m) {
-    most = max(most, groups(s_len[m]));
-    lo_group = min(lo_group, kept(s_len[m], d_len[m]));
+  if (tid == 0) {
+    range[0] = 0x7fffffff;
+    range[1] = 0;
   }
+  __syncthreads();
+  for (int m = m0 + tid; m < m1; m += kReorderThreads) {
+    const int sn = min(max(lens[mv.src_was[m]], 0), g.max_tokens);
+    const int dn = min(max(lens[mv.dst_was[m]], 0), g.max_tokens);
+    s_len[m - m0] = sn;
+    d_len[m - m0] = dn;
+    atomicMin(&range[0], kept(sn, dn));
+    atomicMax(&range[1], groups(sn));
+  }
+  __syncthreads();
+  const int lo_group = range[0], most = range[1];     // groups of the chain: [lo_group, most)
 
   const int upb = g.block_bytes / 16;
   const int64_t tail_units = g.tail_bytes / 16;
   const int64_t sink_units = shared_tokens >= g.sink ? 0 : g.sink_bytes / 16;
-  const int64_t block_units = (int64_t)(most - lo_group) * upb;
-  constexpr int kTile = kReorderThreads * 8;
-  const int64_t bt = (block_units + kTile - 1) / kTile, tt = (tail_units + kTile - 1) / kTile,
-                st = (sink_units + kTile - 1) / kTile;
+  const int64_t bt = ((int64_t)max(most - lo_group, 0) * upb + kReorderTile - 1) / kReorderTile,
+                tt = (tail_units + kReorderTile - 1) / kReorderTile,
+                st = (sink_units + kReorderTile - 1) / kReorderTile;
   const int64_t per_head = bt + tt + st;
 
   for (int64_t tile = blockIdx.x; tile < per_head * g.hkv; tile += gridDim.x) {
@@ -94,50 +124,32 @@ __global__ void __launch_bounds__(kReorderThreads)
     int64_t t = tile % per_head;
     const int area = t < bt ? 0 : t < bt + tt ? 1 : 2;
     t -= area == 0 ? 0 : area == 1 ? bt : bt + tt;
-    const int64_t u0 = t * kTile + tid;
-    const int64_t end = area == 0 ? block_units : area == 1 ? tail_units : sink_units;
+    const uint32_t u0 = (uint32_t)t * kReorderTile + tid;
+    const int64_t per_seq = area == 0   ? (int64_t)g.max_groups * g.block_bytes
+                            : area == 1 ? g.tail_bytes
+                                        : g.sink_bytes;
+    unsigned char* at = cache + (area == 0 ? g.blocks_off + (int64_t)lo_group * g.block_bytes
+                                 : area == 1 ? g.tails_off
+                                             : g.sinks_off) + h * per_seq;
     for (int m = m0; m < m1;) {
       // the batch: consecutive moves with the same number
       int n = 1;
       while (m + n < m1 && mv.batch[m + n] == mv.batch[m]) ++n;
       __syncthreads();
-      if (tid < 2 * n) {
-        const int seq = tid < n ? mv.src[m + tid] : mv.dst[m + tid - n];
-        int64_t off;
-        if (area == 0)
-          off = g.blocks_off + (((int64_t)seq * g.hkv + h) * g.max_groups + lo_group) * g.block_bytes;
-        else if (area == 1)
-          off = g.tails_off + ((int64_t)seq * g.hkv + h) * g.tail_bytes;
-        else
-          off = g.sinks_off + ((int64_t)seq * g.hkv + h) * g.sink_bytes;
-        (tid < n ? s_off[tid] : d_off[tid - n]) = off;
+      if (tid >= n && tid < NB) area_of[tid] = MoveArea{0, 0, 0u, 0u};
+      if (tid < n) {
+        const int sn = s_len[m + tid - m0], dn = d_len[m + tid - m0];
+        MoveArea a;
+        a.src = mv.src[m + tid];
+        a.dst = mv.dst[m + tid];
+        a.lo = area == 0 ? (uint32_t)(kept(sn, dn) - lo_group) * upb : 0u;
+        a.hi = area == 0 ? (uint32_t)(groups(sn) - lo_group) * upb
+                         : sn == 0 ? 0u : (uint32_t)(area == 1 ? tail_units : sink_units);
+        area_of[tid] = a;
       }
       __syncthreads();
-      const int32_t* sl = s_len + (m - m0);
-      const int32_t* dl = d_len + (m - m0);
-      auto live = [&](int k, int64_t u) {
-        if (area != 0) return sl[k] > 0;
-        const int grp = lo_group + (int)(u / upb);
-        if (grp >= groups(sl[k]) || grp < kept(sl[k], dl[k])) return false;
-        if (!g.akvq_delta) return true;
-        return akvq_key_bits(grp, sl[k], g.G, g.akvq_delta) == 4 || (int)(u % upb) * 16 < g.a2_bytes;
-      };
-      if (n <= 2) {
-#pragma unroll 1
-        for (int x = 0; x < 8; x += 4)
-          move_units<2, 4>(cache, s_off, d_off, u0 + (int64_t)x * kReorderThreads, kReorderThreads,
-                           end, n, live);
-      } else if (n <= 4) {
-#pragma unroll 1
-        for (int x = 0; x < 8; x += 2)
-          move_units<4, 2>(cache, s_off, d_off, u0 + (int64_t)x * kReorderThreads, kReorderThreads,
-                           end, n, live);
-      } else {
-#pragma unroll 1
-        for (int x = 0; x < 8; ++x)
-          move_units<8, 1>(cache, s_off, d_off, u0 + (int64_t)x * kReorderThreads, kReorderThreads,
-                           end, n, live);
-      }
+      const int32_t* len = s_len + (m - m0);
+      move_units<NB, kUnits, AK>(g, at, per_seq * g.hkv, area_of, len, u0, n, area == 0, lo_group);
       m += n;
     }
   }
@@ -147,7 +159,7 @@ __global__ void __launch_bounds__(kReorderThreads)
   if (tid == 0) last = atomic_add_acq_rel_gpu(ticket, 1) == (int)gridDim.x - 1;
   __syncthreads();
   if (last) {
-    for (int m = m0 + tid; m < m1; m += kReorderThreads) 
+    for (int m = m0 + tid; m < m1; m += kReorderThreads)
       if (mv.last[m]) lens[mv.dst[m]] = s_len[m - m0];
     if (tid == 0) *ticket = 0;
   }
@@ -156,13 +168,28 @@ __global__ void __launch_bounds__(kReorderThreads)
 }  // namespace
 
 cudaError_t launch_reorder(const Geom& g, unsigned char* cache, const ReorderMoves& mv,
-                           int shared_tokens, int64_t tiles, cudaStream_t stream) {
-  // four resident blocks on each of the 148 SMs are enough loads in flight;
-  // more tiles than that are walked with a stride
+                           int shared_tokens, int64_t bytes, cudaStream_t stream) {
+  int most = 1;
+  for (int i = 0, n = 1; i + 1 < mv.chain_start[mv.n_chains]; ++i) {
+    n = mv.batch[i + 1] == mv.batch[i] ? n + 1 : 1;
+    most = std::max(most, n);
+  }
+  const int nb = most <= 1 ? 1 : most <= 2 ? 2 : most <= 4 ? 4 : 8;
+  // a tile's steps per (kv head, area); four blocks on each of 148 SMs, twice,
+  // and more tiles than that are walked with a stride
+  const int64_t tile = 16LL * kReorderThreads * (8 / nb);
+  const int64_t tiles = g.hkv * (bytes / tile + g.tail_bytes / tile + g.sink_bytes / tile + 3);
   const int64_t want = (148 * 8 + mv.n_chains - 1) / mv.n_chains;
-  const int64_t gx = tiles < want ? tiles : want;
-  reorder_kernel<<<dim3((unsigned)(gx < 1 ? 1 : gx), (unsigned)mv.n_chains), kReorderThreads, 0,
-                   stream>>>(g, cache, mv, shared_tokens);
+  const dim3 grid((unsigned)std::min(tiles, want), (unsigned)mv.n_chains);
+#define KVQ_REORDER(N_)                                                                          \
+  if (nb == N_) {                                                                                \
+    if (g.akvq_delta)                                                                            \
+      reorder_kernel<N_, true><<<grid, kReorderThreads, 0, stream>>>(g, cache, mv, shared_tokens); \
+    else                                                                                         \
+      reorder_kernel<N_, false><<<grid, kReorderThreads, 0, stream>>>(g, cache, mv, shared_tokens); \
+  }
+  KVQ_REORDER(1) KVQ_REORDER(2) KVQ_REORDER(4) KVQ_REORDER(8)
+#undef KVQ_REORDER
   return cudaGetLastError();
 }
 

@@ -192,6 +192,7 @@ class KVQCache:
                                spec.window, spec.sink, spec.rotate, spec.akvq_delta)
         cache_bytes, ws_bytes = required_bytes(self.cfg)
         self.buffer = torch.empty(cache_bytes, dtype=torch.uint8, device=device)
+        self._device = self.buffer.get_device()
         self.workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=device)
         torch.cuda.synchronize(self.buffer.device)
         h = _vp()
@@ -275,27 +276,28 @@ class KVQCache:
         return out
 
     # ---- several new tokens per sequence, positions, reordering ----
-    def _on(self, t: torch.Tensor, name: str, dtype=None) -> torch.Tensor:
-        """t, if it lives on the cache's device (and has the type)."""
-        if t.device != self.buffer.device:
+    def _ptr(self, t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
+        """The address of a contiguous tensor on the cache's device, of the type and shape given."""
+        if t.get_device() != self._device:
             raise ValueError(f"{name} must be on {self.buffer.device}, got {t.device}")
         if dtype is not None and t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        return t
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
 
-    def _launch(self, stream, fn, name, *args):
-        """fn(*args, stream) on the cache's device (the caller's current one stays)."""
-        with torch.cuda.device(self.buffer.device):
-            check(fn(*args, _stream(stream)), name)
-
-    def _rows(self, t: torch.Tensor, name: str, rows: int, heads: int) -> int:
-        """Elements between the rows of t [rows, heads, d], each row's heads side by side."""
-        d = self.spec.head_dim
-        if tuple(t.shape) != (rows, heads, d):
-            raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(t.shape)}")
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-            raise ValueError(f"{name}: a row's heads must lie side by side")
-        return t.stride(0) if rows > 1 else heads * d
+    def _launch(self, name, fn, stream, *args):
+        """fn(*args, stream) on the cache's device; without a stream, on that device's current one."""
+        if torch.cuda.current_device() == self._device:
+            raw = torch._C._cuda_getCurrentRawStream(self._device) if stream is None else stream.cuda_stream
+            status = fn(*args, raw)
+        else:
+            with torch.cuda.device(self._device):
+                status = fn(*args, _stream(stream))
+        if status != KVQ_OK:
+            raise KvqError(status, name)
 
     def attend(self, q: torch.Tensor, n_q, scale: float = 0.0, cap: float = 0.0, window: int = 0,
                slopes: torch.Tensor | None = None, prefix: torch.Tensor | None = None,
@@ -305,28 +307,33 @@ class KVQCache:
         q: [sum(n_q), n_q_heads, d]; scale (0: 1 / sqrt(d)), cap, window: numbers, 0 for none;
         slopes: fp32 [n_q_heads], prefix: int32 [n_seq], on the device.  Returns fp16 like q.
         """
-        if q.dtype not in DTYPE_CODES:
+        dt = DTYPE_CODES.get(q.dtype)
+        if dt is None:
             raise ValueError("q must be fp16, bf16 or fp32")
-        n_q = [int(x) for x in n_q]
-        want = (sum(n_q), self.spec.n_q_heads, self.spec.head_dim)
-        if tuple(q.shape) != want:
-            raise ValueError(f"q must be {want}, got {tuple(q.shape)}")
-        self._on(q, "q")
-        if slopes is not None and tuple(self._on(slopes, "slopes", torch.float32).shape) != want[1:2]:
-            raise ValueError(f"slopes must be [{want[1]}]")
-        if prefix is not None and tuple(self._on(prefix, "prefix", torch.int32).shape) != (len(n_q),):
-            raise ValueError(f"prefix must be [{len(n_q)}]")
+        sp, n_seq = self.spec, len(n_q)
+        arr = (ctypes.c_int32 * n_seq)(*n_q)
+        shape = (sum(n_q), sp.n_q_heads, sp.head_dim)
+        qp = self._ptr(q, "q", None, shape)
+        sc = KvqScores(scale, cap, window,
+                       None if slopes is None else self._ptr(slopes, "slopes", torch.float32, (sp.n_q_heads,)),
+                       None if prefix is None else self._ptr(prefix, "prefix", torch.int32, (n_seq,)))
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
-        elif self._on(out, "out", torch.float16).shape != q.shape:
-            raise ValueError("out must be shaped like q")
-        sc = KvqScores(scale, cap, window, None if slopes is None else _dev_ptr(slopes, "slopes"),
-                       None if prefix is None else _dev_ptr(prefix, "prefix"))
-        arr = (ctypes.c_int32 * len(n_q))(*n_q)
-        self._launch(stream, kvq_attend, "kvq_attend", self._h, _dev_ptr(q, "q"), DTYPE_CODES[q.dtype],
-                     arr, len(n_q), ctypes.byref(sc), _dev_ptr(out, "out"), self.workspace.data_ptr(),
+            out = torch.empty(shape, dtype=torch.float16, device=q.device)
+        self._launch("kvq_attend", kvq_attend, stream, self._h, qp, dt, arr, n_seq, ctypes.byref(sc),
+                     self._ptr(out, "out", torch.float16, shape), self.workspace.data_ptr(),
                      self.workspace.numel())
         return out
+
+    def _rows(self, t: torch.Tensor, name: str, dtype, shape) -> tuple[int, int]:
+        """Address of t [rows, heads, d] with each row's heads side by side, and elements between rows."""
+        if t.get_device() != self._device or t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype} on {self.buffer.device}, got {t.dtype} on {t.device}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        st = t.stride()
+        if t.numel() and (st[2] != 1 or (shape[1] > 1 and st[1] != shape[2])):
+            raise ValueError(f"{name}: a row's heads must lie side by side")
+        return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
 
     def norm_rotary(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None, n_new,
                     inv_freq: torch.Tensor, q_weight: torch.Tensor | None = None,
@@ -342,55 +349,52 @@ class KVQCache:
         [axes, rows] with the pairs of each axis in ``sections``.  Returns contiguous (q, k, v) of
         ``out_dtype`` (v None if it was), written to ``out`` if three tensors are given.
         """
-        if q.dtype not in DTYPE_CODES or out_dtype not in DTYPE_CODES:
+        dt, odt = DTYPE_CODES.get(q.dtype), DTYPE_CODES.get(out_dtype)
+        if dt is None or odt is None:
             raise ValueError("rows and outputs must be fp16, bf16 or fp32")
-        n_new = [int(x) for x in n_new]
-        n, sp = sum(n_new), self.spec
-        parts = [(q, "q", sp.n_q_heads), (k, "k", sp.n_kv_heads), (v, "v", sp.n_kv_heads)]
-        strides = [0 if t is None else self._rows(self._on(t, m, q.dtype), m, n, h) for t, m, h in parts]
-        if out is None:
-            out = [None if t is None else torch.empty((n, h, sp.head_dim), dtype=out_dtype, device=t.device)
-                   for t, _, h in parts]
-        for t, o, (_, m, h) in zip((q, k, v), out, parts):
-            if (t is None) != (o is None):
-                raise ValueError(f"{m} and its output go together")
-            if o is not None and tuple(self._on(o, m + " output", out_dtype).shape) != (n, h, sp.head_dim):
-                raise ValueError(f"{m} output must be [{n}, {h}, {sp.head_dim}]")
-        for t, m in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if t is not None and tuple(self._on(t, m, q.dtype).shape) != (sp.head_dim,):
-                raise ValueError(f"{m} must be [{sp.head_dim}]")
-        if self._on(inv_freq, "inv_freq", torch.float32).dim() != 1:
+        sp, n, n_seq, d, kind = self.spec, sum(n_new), len(n_new), self.spec.head_dim, q.dtype
+        arr = (ctypes.c_int32 * n_seq)(*n_new)
+        q_shape, k_shape = (n, sp.n_q_heads, d), (n, sp.n_kv_heads, d)
+        qp, qs = self._rows(q, "q", kind, q_shape)
+        kp, ks = self._rows(k, "k", kind, k_shape)
+        vp, vs = (None, 0) if v is None else self._rows(v, "v", kind, k_shape)
+        if inv_freq.dim() != 1:
             raise ValueError("inv_freq must be [pairs]")
-        rot = KvqRotary(inv_freq=_dev_ptr(inv_freq, "inv_freq"), n_pairs=inv_freq.numel(),
-                        interleaved=int(interleaved), eps=eps,
-                        q_weight=None if q_weight is None else _dev_ptr(q_weight, "q_weight"),
-                        k_weight=None if k_weight is None else _dev_ptr(k_weight, "k_weight"))
+        pairs = inv_freq.numel()
+        rot = KvqRotary(self._ptr(inv_freq, "inv_freq", torch.float32), pairs, int(interleaved), None, 0,
+                        (0, 0, 0, 0),
+                        None if q_weight is None else self._ptr(q_weight, "q_weight", kind, (d,)),
+                        None if k_weight is None else self._ptr(k_weight, "k_weight", kind, (d,)), eps)
         if positions is not None:
             axes = positions.shape[0] if positions.dim() == 2 else 1
             if positions.dim() not in (1, 2) or positions.shape[-1] != n or not 1 <= axes <= 4:
                 raise ValueError(f"positions must be [{n}] or [1 to 4 axes, {n}]")
-            sections = [inv_freq.numel()] if sections is None and axes == 1 else list(sections or [])
+            sections = [pairs] if sections is None and axes == 1 else list(sections or [])
             if len(sections) != axes:
                 raise ValueError(f"sections must give the pairs of {axes} axes")
-            rot.positions = _dev_ptr(self._on(positions, "positions", torch.int32), "positions")
+            rot.positions = self._ptr(positions, "positions", torch.int32)
             rot.n_axes = axes
-            rot.sections[:axes] = [int(x) for x in sections]
+            rot.sections[:axes] = sections
         elif sections is not None:
             raise ValueError("sections go with positions")
-        ptr = [None if t is None else t.data_ptr() for t in (q, k, v)]
-        dst = [None if t is None else _dev_ptr(t, "out") for t in out]
-        arr = (ctypes.c_int32 * len(n_new))(*n_new)
-        self._launch(stream, kvq_norm_rotary, "kvq_norm_rotary", self._h, ptr[0], strides[0], ptr[1],
-                     strides[1], ptr[2], strides[2], DTYPE_CODES[q.dtype], arr, len(n_new),
-                     ctypes.byref(rot), *dst, DTYPE_CODES[out_dtype])
-        return tuple(out)
+        if out is None:
+            dev = q.device
+            out = (torch.empty(q_shape, dtype=out_dtype, device=dev), torch.empty(k_shape, dtype=out_dtype, device=dev),
+                   None if v is None else torch.empty(k_shape, dtype=out_dtype, device=dev))
+        qo, ko, vo = out
+        if qo is None or ko is None or (vo is None) != (v is None):
+            raise ValueError("out must hold a tensor for each of q, k and v")
+        self._launch("kvq_norm_rotary", kvq_norm_rotary, stream, self._h, qp, qs, kp, ks, vp, vs, dt, arr, n_seq,
+                     ctypes.byref(rot), self._ptr(qo, "q output", out_dtype, q_shape),
+                     self._ptr(ko, "k output", out_dtype, k_shape),
+                     None if vo is None else self._ptr(vo, "v output", out_dtype, k_shape), odt)
+        return qo, ko, vo
 
     def reorder(self, parent, shared: int = 0, stream=None):
         """Sequence b takes over sequence ``parent[b]``, all at once (kvq_reorder); the first
         ``shared`` tokens of moving sequences and their parents are the same already."""
-        parent = [int(x) for x in parent]
-        arr = (ctypes.c_int32 * len(parent))(*parent)
-        self._launch(stream, kvq_reorder, "kvq_reorder", self._h, arr, len(parent), int(shared))
+        n_seq = len(parent)
+        self._launch("kvq_reorder", kvq_reorder, stream, self._h, (ctypes.c_int32 * n_seq)(*parent), n_seq, int(shared))
 
     def workspace_status(self, stream=None) -> int:
         return kvq_workspace_status(self.workspace.data_ptr(), _stream(stream))

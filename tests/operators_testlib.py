@@ -49,9 +49,9 @@ cudaError_t launch_norm_rotary(int, int, int, const RotaryArgs&, const RotarySeq
   for (int i = 0; i < s.n; ++i) put({s.row_off[i]});
   return cudaSuccess;
 }
-cudaError_t launch_reorder(const Geom&, unsigned char*, const ReorderMoves& m, int shared, int64_t tiles, cudaStream_t) {
+cudaError_t launch_reorder(const Geom&, unsigned char*, const ReorderMoves& m, int shared, int64_t bytes, cudaStream_t) {
   const int n = m.chain_start[m.n_chains];
-  put({2, m.n_chains, n, shared, (int32_t)tiles});
+  put({2, m.n_chains, n, shared, (int32_t)bytes});
   for (int i = 0; i <= m.n_chains; ++i) put({m.chain_start[i]});
   for (int i = 0; i < n; ++i) put({m.src[i], m.dst[i], m.src_was[i], m.dst_was[i], m.batch[i], m.last[i]});
   return cudaSuccess;

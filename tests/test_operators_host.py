@@ -166,8 +166,8 @@ def _replay(log, n_all, lens):
     held, lens = list(range(n_all)), list(lens)
     most = 0
     while log:
-        kind, chains, n, shared, tiles = log[:5]
-        assert kind == 2 and tiles >= 1
+        kind, chains, n, shared, size = log[:5]
+        assert kind == 2 and size >= 0
         start, log = log[5:6 + chains], log[6 + chains:]
         moves, log = [log[6 * i:6 * i + 6] for i in range(n)], log[6 * n:]
         most = max(most, n)

@@ -6,36 +6,37 @@
 namespace kvq {
 namespace {
 
-constexpr int kMergeThreads = 32 * kAttendRows;
+constexpr int kMergeWarps = 4;
 
-// Merges the pieces of split units, a warp per row: blocks are (piece, eight
-// rows of the unit), of which those of a unit's first piece do the work (the
-// others leave at once).  With the rows' maxima m_i and sums l_i relative to
-// them, out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// Merges the pieces of split units: a block is a row (x: unit, y: row of the
+// unit), its warps take every fourth piece.  With the pieces' maxima m_i and
+// sums l_i relative to them, out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m)
+// l_i.  (One warp for all of a row's pieces took 20 us for the 74 pieces of a
+// 128k context.)
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(32 * kMergeWarps)
     attend_merge_kernel(const Geom g, const WsLayout w, const AttendArgs a, const AttendSeqs seqs) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int V = D / 32;
+  __shared__ float part[kMergeWarps][D + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int lo = 0, hi = seqs.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (seqs.piece_off[mid] <= (int)blockIdx.x) lo = mid; else hi = mid;
+    if (seqs.unit_off[mid] <= (int)blockIdx.x) lo = mid; else hi = mid;
   }
   const int R = seqs.n_q[lo] * g.gqa, tiles = (R + seqs.unit_rows - 1) / seqs.unit_rows;
-  const int local = blockIdx.x - seqs.piece_off[lo];
+  const int unit = blockIdx.x - seqs.unit_off[lo];        // of the sequence
   const int parts = (seqs.piece_off[lo + 1] - seqs.piece_off[lo]) / (g.hkv * tiles);
-  const int h = local / parts / tiles, tile = local / parts % tiles;
-  const int ur = blockIdx.y * kAttendRows + warp;        // row of the unit
+  const int h = unit / tiles, tile = unit % tiles, ur = blockIdx.y;
   // (the tensor-core kernel numbers a sequence's row tiles from the last)
   const int r = (seqs.unit_rows == kAttendRows ? tile : tiles - 1 - tile) * seqs.unit_rows + ur;
-  if (parts < 2 || local % parts != 0 || r >= R) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (parts < 2 || r >= R) return;
   const float* ps = reinterpret_cast<const float*>(a.ws + w.partials_off) +
-                    ((int64_t)blockIdx.x * seqs.slot_rows + ur) * (D + 4);
-  const int64_t kStep = (int64_t)seqs.slot_rows * (D + 4);
+                    ((int64_t)(seqs.piece_off[lo] + unit * parts) * seqs.slot_rows + ur) * (D + 4);
+  const int64_t step = (int64_t)seqs.slot_rows * (D + 4);
   float m = -INFINITY;
-  for (int s = lane; s < parts; s += 32) m = fmaxf(m, ps[s * kStep + D]);
+  for (int s = lane; s < parts; s += 32) m = fmaxf(m, ps[s * step + D]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float base = m == -INFINITY ? 0.f : m;
@@ -43,13 +44,25 @@ __global__ void __launch_bounds__(kMergeThreads)
 #pragma unroll
   for (int i = 0; i < V; ++i) y[i] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float* p = ps + s * kStep;
+  for (int s = warp; s < parts; s += kMergeWarps) {
+    const float* p = ps + s * step;
     const float f = fast_exp2(p[D] - base);
     l += f * p[D + 1];
 #pragma unroll
     for (int i = 0; i < V; ++i) y[i] += f * p[lane * V + i];
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) part[warp][lane * V + i] = y[i];
+  if (lane == 0) part[warp][D] = l;
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int x = 1; x < kMergeWarps; ++x) {
+    l += part[x][D];
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] += part[x][lane * V + i];
+  }
+  l = __shfl_sync(0xffffffffu, l, 0);
   attend_store_row<D>(g, a, seqs, lo, h, r, y, l, lane);
 }
 
@@ -74,8 +87,8 @@ cudaError_t launch_attend(const Geom& g, const WsLayout& w, const AttendArgs& a,
 #undef KVQ_CASE
   if (e != cudaSuccess || !split) return e;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)s.piece_off[s.n], (unsigned)((s.slot_rows + kAttendRows - 1) / kAttendRows));
-  lc.blockDim = dim3(kMergeThreads);
+  lc.gridDim = dim3((unsigned)s.unit_off[s.n], (unsigned)s.slot_rows);
+  lc.blockDim = dim3(32 * kMergeWarps);
   lc.stream = stream;
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -408,6 +408,8 @@ __global__ void __launch_bounds__(kAttThreads, 4)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2;
   int32_t* err = reinterpret_cast<int32_t*>(a.ws + w.err_off);
 
+  // the merge of split units may be launched (it waits for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // ---- this piece: sequence, kv head, row tile, part of the key list
   int sq;
   {

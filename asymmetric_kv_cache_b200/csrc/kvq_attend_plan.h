@@ -28,7 +28,7 @@ inline bool plan_attend(const Geom& g, const int32_t* lens, const int32_t* n_q, 
   out->n = n;
   out->seq0 = s0;
   out->unit_rows = unit_rows;
-  out->slot_rows = kAttendRows;
+  out->slot_rows = 1;
   const bool tc = unit_rows > kAttendRows;
   const int step = tc ? 64 : g.G;        // keys of one step of the kernel
   auto rows = [&](int b) {
@@ -48,16 +48,17 @@ inline bool plan_attend(const Geom& g, const int32_t* lens, const int32_t* n_q, 
     cost += u * steps(b);
     if (u > 0)
       out->slot_rows = (int)std::max<int64_t>(
-          out->slot_rows, (std::min<int64_t>(rows(b), unit_rows) + kAttendRows - 1) / kAttendRows * kAttendRows);
+          out->slot_rows, std::min<int64_t>(rows(b), unit_rows));
   }
   const int64_t want = std::min<int64_t>(max_ctas, kAttendPartialRows / out->slot_rows - units);
-  int64_t pieces = 0, row = row0;
+  int64_t pieces = 0, before = 0, row = row0;
   bool split = false;
   for (int i = 0; i < n; ++i) {
     const int b = s0 + i;
     out->row_off[i] = (int32_t)row;
     out->n_q[i] = n_q[b];
     out->piece_off[i] = (int32_t)pieces;
+    out->unit_off[i] = (int32_t)before;
     row += n_q[b];
     int64_t parts = 1;
     if (units < want && tiles(b) > 0) {
@@ -66,8 +67,10 @@ inline bool plan_attend(const Geom& g, const int32_t* lens, const int32_t* n_q, 
       split |= parts > 1;
     }
     pieces += g.hkv * tiles(b) * parts;
+    before += g.hkv * tiles(b);
   }
   out->piece_off[n] = (int32_t)pieces;
+  out->unit_off[n] = (int32_t)before;
   return split;
 }
 

@@ -304,6 +304,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int32_t* err = reinterpret_cast<int32_t*>(a.ws + w.err_off);
 
+  // the merge of split units may be launched (it waits for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // ---- this piece
   int sq;
   {

@@ -273,6 +273,7 @@ struct AttendSeqs {
   int32_t row_off[kAttendMaxSeqs];
   int32_t n_q[kAttendMaxSeqs];
   int32_t piece_off[kAttendMaxSeqs + 1];
+  int32_t unit_off[kAttendMaxSeqs + 1];   // units before the sequence's
 };
 
 cudaError_t attend_max_ctas(const Geom& g, int* max_ctas);

@@ -85,7 +85,7 @@ cudaError_t launch_attend(const Geom& g, const WsLayout& w, const AttendArgs& a,
     e = launch_attend_##D_##_##KB_##_##VB_##_##G_(g, w, a, s, stream);
   KVQ_DECODE_FOR_EACH(KVQ_CASE)
 #undef KVQ_CASE
-  if (e != cudaSuccess || !split) return e;
+  if (e != cudaSuccess || !split || s.merge_here) return e;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)s.unit_off[s.n], (unsigned)s.slot_rows);
   lc.blockDim = dim3(32 * kMergeWarps);

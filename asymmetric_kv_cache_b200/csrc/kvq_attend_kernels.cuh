@@ -184,6 +184,36 @@ __device__ __forceinline__ bool att_visible(const RowRule& rr, int j) {
   return (j <= rr.pos && rr.pos - j < rr.window) || j < rr.prefix;
 }
 
+// V (2 or 4) consecutive query values.
+template <int V>
+__device__ __forceinline__ void att_load_q(const void* q, int64_t at, int dtype, float (&y)[V]) {
+  if (dtype == KVQ_FP32) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 f = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(q) + at + i);
+      y[i] = f.x;
+      y[i + 1] = f.y;
+    }
+    return;
+  }
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(q) + at);
+  uint32_t w[V / 2];
+  if constexpr (V == 4) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+    w[0] = *p;
+  }
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const float2 f = dtype == KVQ_FP16 ? __half22float2(u32_as_h2(w[i]))
+                                       : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    y[2 * i] = f.x;
+    y[2 * i + 1] = f.y;
+  }
+}
+
 template <int MT>
 struct AttState {
   float o[MT][4];   // O^T: channels 16 mt + g8 (+ 8), rows 2 i4, 2 i4 + 1
@@ -408,8 +438,10 @@ __global__ void __launch_bounds__(kAttThreads, 4)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2;
   int32_t* err = reinterpret_cast<int32_t*>(a.ws + w.err_off);
 
-  // the merge of split units may be launched (it waits for this grid's end)
+  // the next kernel may be launched (it waits for this grid's end), and this
+  // one's CTAs may be resident before the one ahead of it has ended
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this piece: sequence, kv head, row tile, part of the key list
   int sq;
   {
@@ -476,6 +508,7 @@ __global__ void __launch_bounds__(kAttThreads, 4)
   // but with at most 4 rows the upper 4 repeat the lower ones.
   {
     constexpr int V = D / 32;
+#pragma unroll
     for (int x = 0; x < kAttendRows / kAttWarps; ++x) {
       const int r = warp * (kAttendRows / kAttWarps) + x, rs = dup ? r & 3 : r;
       float y[V];
@@ -484,8 +517,7 @@ __global__ void __launch_bounds__(kAttThreads, 4)
       if (rs < nr) {
         const int qi = (r0 + rs) / g.gqa, hh = (r0 + rs) % g.gqa;
         const int64_t at = ((int64_t)(seqs.row_off[sq] + qi) * g.hq + h * g.gqa + hh) * D + lane * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) y[i] = load_as_float(a.q, at + i, a.q_dtype);
+        att_load_q<V>(a.q, at, a.q_dtype, y);
       }
       if (g.rotate) {
         fwht_lanes<D, V>(y, lane);
@@ -632,6 +664,52 @@ __global__ void __launch_bounds__(kAttThreads, 4)
     } else {
       attend_store_row<D>(g, a, seqs, sq, h, r0 + r, y, l, lane);
     }
+  }
+  if (parts == 1 || !seqs.merge_here) return;
+
+  // ---- the last piece of the unit to end merges them all (a few pieces: the
+  // launch of a merge kernel would take longer).  Read past the first-level
+  // cache, which may hold a neighbouring unit's sector from before.
+  __shared__ int32_t last;
+  const int unit = local / parts;
+  __syncthreads();
+  if (tid == 0) {
+    int* ticket = reinterpret_cast<int*>(a.ws + w.att_tickets_off) + seqs.unit_off[sq] + unit;
+    __threadfence();
+    last = atomic_add_acq_rel_gpu(ticket, 1) == parts - 1;
+    if (last) *ticket = 0;
+  }
+  __syncthreads();
+  if (!last) return;
+  const int64_t step = (int64_t)seqs.slot_rows * (D + 4);
+  for (int r = warp; r < nr; r += kAttWarps) {
+    const float* ps = reinterpret_cast<const float*>(a.ws + w.partials_off) +
+                      ((int64_t)(blockIdx.x - part) * seqs.slot_rows + r) * (D + 4);
+    float m = lane < parts ? __ldcg(ps + lane * step + D) : -INFINITY;
+    float l = lane < parts ? __ldcg(ps + lane * step + D + 1) : 0.f;
+    float top = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = fast_exp2(m - (top == -INFINITY ? 0.f : top));   // of piece `lane`
+    l *= f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float y[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < parts; ++s) {
+      const float fs = __shfl_sync(0xffffffffu, f, s);
+      const float* p = ps + s * step + lane * V;
+      if constexpr (V == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+        y[0] += fs * x.x; y[1] += fs * x.y; y[2] += fs * x.z; y[3] += fs * x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+        y[0] += fs * x.x; y[1] += fs * x.y;
+      }
+    }
+    attend_store_row<D>(g, a, seqs, sq, h, r0 + r, y, l, lane);
   }
 }
 

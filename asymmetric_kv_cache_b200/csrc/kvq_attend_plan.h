@@ -50,9 +50,11 @@ inline bool plan_attend(const Geom& g, const int32_t* lens, const int32_t* n_q, 
       out->slot_rows = (int)std::max<int64_t>(
           out->slot_rows, std::min<int64_t>(rows(b), unit_rows));
   }
-  const int64_t want = std::min<int64_t>(max_ctas, kAttendPartialRows / out->slot_rows - units);
+  const int64_t want = units < kAttendTickets
+                           ? std::min<int64_t>(max_ctas, kAttendPartialRows / out->slot_rows - units)
+                           : 0;
+  int64_t most = 1;
   int64_t pieces = 0, before = 0, row = row0;
-  bool split = false;
   for (int i = 0; i < n; ++i) {
     const int b = s0 + i;
     out->row_off[i] = (int32_t)row;
@@ -64,14 +66,15 @@ inline bool plan_attend(const Geom& g, const int32_t* lens, const int32_t* n_q, 
     if (units < want && tiles(b) > 0) {
       parts = steps(b) * want / cost;
       parts = std::max<int64_t>(1, std::min(parts, (steps(b) + 3) / 4));
-      split |= parts > 1;
+      most = std::max(most, parts);
     }
     pieces += g.hkv * tiles(b) * parts;
     before += g.hkv * tiles(b);
   }
   out->piece_off[n] = (int32_t)pieces;
   out->unit_off[n] = (int32_t)before;
-  return split;
+  out->merge_here = !tc && most <= kAttendMergeParts;
+  return most > 1;
 }
 
 }  // namespace kvq

@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int32_t* err = reinterpret_cast<int32_t*>(a.ws + w.err_off);
 
-  // the merge of split units may be launched (it waits for this grid's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this piece
   int sq;
   {
@@ -385,8 +385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int k = 0; k < V; ++k) y[k] = 0.f;
       if (wrow + i < nr) {
         const int64_t at = ((int64_t)(seqs.row_off[sq] + r / g.gqa) * g.hq + h * g.gqa + r % g.gqa) * D + lane * V;
-#pragma unroll
-        for (int k = 0; k < V; ++k) y[k] = load_as_float(a.q, at + k, a.q_dtype);
+        att_load_q<V>(a.q, at, a.q_dtype, y);
       }
       if (g.rotate) {
         fwht_lanes<D, V>(y, lane);
@@ -721,6 +720,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
+// A launch that may begin while the kernel before it ends (it waits for its
+// memory in the kernel).
+template <class Kernel>
+cudaError_t attend_launch(Kernel kernel, int grid, int threads, size_t smem, cudaStream_t stream,
+                          const Geom& g, const WsLayout& w, const AttendArgs& a, const AttendSeqs& s) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = la;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, g, w, a, s);
+}
+
 template <int D, int KB, int VB, int G>
 cudaError_t launch_attend_tc_t(const Geom& g, const WsLayout& w, const AttendArgs& a,
                                const AttendSeqs& s, cudaStream_t stream) {
@@ -740,9 +757,8 @@ cudaError_t launch_attend_tc_t(const Geom& g, const WsLayout& w, const AttendArg
     if (fa.numRegs < kTcRegs) return cudaErrorInvalidKernelImage;
     ready.fetch_or(1ull << (dev & 63));
   }
-  attend_tc_kernel<D, KB, VB, G>
-      <<<(unsigned)s.piece_off[s.n], kTcThreads, TcAtt<D>::SMEM, stream>>>(g, w, a, s);
-  return cudaGetLastError();
+  return attend_launch(attend_tc_kernel<D, KB, VB, G>, s.piece_off[s.n], kTcThreads, TcAtt<D>::SMEM, stream, g, w,
+                       a, s);
 }
 
 template <int D, int KB, int VB, int G>
@@ -753,8 +769,7 @@ cudaError_t launch_attend_t(const Geom& g, const WsLayout& w, const AttendArgs& 
   if (s.unit_rows != kAttendRows) return launch_attend_tc_t<D, KB, VB, G>(g, w, a, s, stream);
   cudaError_t e = attend_configure<D, KB, VB, G>();
   if (e != cudaSuccess) return e;
-  attend_kernel<D, KB, VB, G><<<(unsigned)s.piece_off[s.n], kAttThreads, C::SMEM, stream>>>(g, w, a, s);
-  return cudaGetLastError();
+  return attend_launch(attend_kernel<D, KB, VB, G>, s.piece_off[s.n], kAttThreads, C::SMEM, stream, g, w, a, s);
 }
 
 #define KVQ_ATTEND_DEFINE(D_, KB_, VB_, G_)                                                       \

@@ -49,6 +49,7 @@ struct Geom {
 // last CTA to finish merges them (it resets the ticket to 0).
 struct WsLayout {
   int64_t err_off, units_off, tickets_off, partials_off, total;
+  int64_t att_tickets_off;   // kvq_attend's tickets (caches' workspaces), zero between calls
   int32_t units;       // split records
   int32_t slot_floats; // floats per partial slot: heads x (o[d], m, l, 2 pad)
 };
@@ -241,13 +242,18 @@ constexpr int kAttendRows = 8;
 // Rows (D + 4 floats each) that the partials of one launch's split units may
 // take in a cache's workspace: 148 tensor-core units of 256 rows.
 constexpr int kAttendPartialRows = 148 * 256;
+// Units that a launch cuts into pieces at most (their tickets), and pieces of
+// a unit up to which the last of them to end merges them all.
+constexpr int kAttendTickets = 4096;
+constexpr int kAttendMergeParts = 32;
 // From this many rows per kv head on a sequence goes to the tensor-core kernel.
 constexpr int kAttendTcRows = 64;
 
 inline void make_cache_ws_layout(const Geom& g, WsLayout* w) {
   make_ws_layout(g, w);
   const int64_t end = align_up(w->partials_off + 4LL * kAttendPartialRows * (g.d + 4), 256);
-  if (end > w->total) w->total = end;
+  w->att_tickets_off = end > w->total ? end : w->total;
+  w->total = align_up(w->att_tickets_off + 4LL * kAttendTickets, 256);
 }
 
 struct AttendArgs {
@@ -270,6 +276,7 @@ struct AttendSeqs {
   int32_t n, seq0;
   int32_t unit_rows;         // kAttendRows, or 256 / 128 (tensor cores)
   int32_t slot_rows;         // rows of a piece's partial slot
+  int32_t merge_here;        // the last piece of a unit merges them (no merge kernel)
   int32_t row_off[kAttendMaxSeqs];
   int32_t n_q[kAttendMaxSeqs];
   int32_t piece_off[kAttendMaxSeqs + 1];

@@ -87,7 +87,7 @@ def test_attend_plan(host, seed, dt):
                 cut = True
                 assert got // units <= (lens[b] // (64 if unit > 8 else 32) + 4) // 4 and slot >= min(rows, unit)
         assert cut == bool(split)
-        assert not split or pieces * slot * (128 + 4) * 4 <= host.ws - 512
+        assert not split or pieces * slot * (128 + 4) * 4 <= host.ws - 4 * 4096 - 512
     assert sorted(seen) == [b for b in range(seqs) if n_q[b]]
 
 

@@ -471,6 +471,9 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   a.prefix = sc.prefix;
   // fp32 and rotated queries are not fp16 numbers: value and residual parts
   a.residual = q_dtype == KVQ_FP32 || g.rotate;
+  int tc_rows = kvq::attend_tc_rows(g, cache->lens.data(), n_q, n_seq, sc.window);
+  if (const char* env = std::getenv("KVQ_ATTEND_TC"); env && (env[0] == '0' || env[0] == '1') && !env[1])
+    tc_rows = env[0] == '1' ? 1 : INT32_MAX;
   static thread_local kvq::AttendSeqs seqs;
   int64_t row = 0;
   for (int s0 = 0; s0 < n_seq; s0 += kvq::kAttendMaxSeqs) {
@@ -478,7 +481,7 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
     for (int tc = 1; tc >= 0; --tc) {
       const int unit_rows = !tc ? kvq::kAttendRows : a.residual ? 128 : 256;
       const bool split = kvq::plan_attend(g, cache->lens.data(), n_q, s0, n, sc.window,
-                                          cache->attend_ctas[tc], unit_rows, row, &seqs);
+                                          cache->attend_ctas[tc], tc_rows, unit_rows, row, &seqs);
       if (seqs.piece_off[n] == 0) continue;
       cudaError_t e = kvq::launch_attend(g, cache->ws, a, seqs, split, (cudaStream_t)stream);
       if (e != cudaSuccess) return cuda_fail(e, "attend launch");

@@ -8,11 +8,25 @@
 
 namespace kvq {
 
-// The launch of sequences [s0, s0 + n), of which those with at least
-// kAttendTcRows rows per kv head belong to the tensor-core kernel (unit_rows >
-// kAttendRows) and the others to the register-tile kernel; the launch of
-// either kernel skips the other's.  row0: the first sequence's first query
-// row.
+// The rows per kv head from which on the call's sequences go to the
+// tensor-core kernel (INT32_MAX: none does).
+inline int attend_tc_rows(const Geom& g, const int32_t* lens, const int32_t* n_q, int n_seq,
+                          int score_window) {
+  int64_t steps = 0;
+  for (int b = 0; b < n_seq; ++b) {
+    const int64_t rows = (int64_t)n_q[b] * g.gqa;
+    if (rows < kAttendTcRows) continue;
+    int64_t keys = lens[b];
+    if (score_window > 0) keys = std::min<int64_t>(keys, (int64_t)score_window + n_q[b]);
+    steps += g.hkv * ((rows + 7) / 8) * (keys / 32 + 1) * g.d / 128;
+  }
+  return steps >= kAttendTcSteps ? kAttendTcRows : INT32_MAX;
+}
+
+// The launch of sequences [s0, s0 + n), of which those with at least tc_rows
+// rows per kv head belong to the tensor-core kernel (unit_rows > kAttendRows)
+// and the others to the register-tile kernel; the launch of either kernel
+// skips the other's.  row0: the first sequence's first query row.
 //
 // A unit is (sequence, kv head, tile of unit_rows rows).  With at least as
 // many units as resident CTAs every unit is one piece.  Otherwise the units
@@ -23,7 +37,7 @@ namespace kvq {
 // so a replayed launch stays right when they have grown.  Returns whether
 // some unit is cut.
 inline bool plan_attend(const Geom& g, const int32_t* lens, const int32_t* n_q, int s0, int n,
-                        int score_window, int max_ctas, int unit_rows, int64_t row0,
+                        int score_window, int max_ctas, int tc_rows, int unit_rows, int64_t row0,
                         AttendSeqs* out) {
   out->n = n;
   out->seq0 = s0;
@@ -33,7 +47,7 @@ inline bool plan_attend(const Geom& g, const int32_t* lens, const int32_t* n_q, 
   const int step = tc ? 64 : g.G;        // keys of one step of the kernel
   auto rows = [&](int b) {
     const int64_t r = (int64_t)n_q[b] * g.gqa;
-    return tc == (r >= kAttendTcRows) ? r : 0;
+    return tc == (r >= tc_rows) ? r : 0;
   };
   auto tiles = [&](int b) { return (rows(b) + unit_rows - 1) / unit_rows; };
   auto steps = [&](int b) {

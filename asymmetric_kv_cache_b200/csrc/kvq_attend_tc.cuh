@@ -378,27 +378,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   unsigned char* io = smem + (warp & 7) * 32 * C::IO_ROW;
   if (warp < 8 && X < nx) {
     constexpr int V = D / 32;
-    for (int i = 0; i < 32; ++i) {
-      const int r = r0 + wrow + i;
-      float y[V];
+    // eight rows' loads at a time
+    for (int i0 = 0; i0 < 32; i0 += 8) {
+      float y[8][V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) y[k] = 0.f;
-      if (wrow + i < nr) {
-        const int64_t at = ((int64_t)(seqs.row_off[sq] + r / g.gqa) * g.hq + h * g.gqa + r % g.gqa) * D + lane * V;
-        att_load_q<V>(a.q, at, a.q_dtype, y);
-      }
-      if (g.rotate) {
-        fwht_lanes<D, V>(y, lane);
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + wrow + i0 + i;
 #pragma unroll
-        for (int k = 0; k < V; ++k) y[k] *= rot_scale<D>();
+        for (int k = 0; k < V; ++k) y[i][k] = 0.f;
+        if (wrow + i0 + i < nr)
+          att_load_q<V>(a.q, ((int64_t)(seqs.row_off[sq] + r / g.gqa) * g.hq + h * g.gqa + r % g.gqa) * D + lane * V,
+                        a.q_dtype, y[i]);
       }
 #pragma unroll
-      for (int k = 0; k < V; k += 2) {
-        const uint32_t hi = pack_h2(y[k], y[k + 1]);
-        const float2 f = __half22float2(u32_as_h2(hi));
-        uint32_t* dst = reinterpret_cast<uint32_t*>(io + i * C::IO_ROW) + (lane * V + k) / 2;
-        dst[0] = hi;
-        dst[D / 2] = pack_h2(y[k] - f.x, y[k + 1] - f.y);
+      for (int i = 0; i < 8; ++i) {
+        if (g.rotate) {
+          fwht_lanes<D, V>(y[i], lane);
+#pragma unroll
+          for (int k = 0; k < V; ++k) y[i][k] *= rot_scale<D>();
+        }
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          const uint32_t hi = pack_h2(y[i][k], y[i][k + 1]);
+          const float2 f = __half22float2(u32_as_h2(hi));
+          uint32_t* dst = reinterpret_cast<uint32_t*>(io + (i0 + i) * C::IO_ROW) + (lane * V + k) / 2;
+          dst[0] = hi;
+          dst[D / 2] = pack_h2(y[i][k] - f.x, y[i][k + 1] - f.y);
+        }
       }
     }
   }

@@ -246,8 +246,16 @@ constexpr int kAttendPartialRows = 148 * 256;
 // a unit up to which the last of them to end merges them all.
 constexpr int kAttendTickets = 4096;
 constexpr int kAttendMergeParts = 32;
-// From this many rows per kv head on a sequence goes to the tensor-core kernel.
-constexpr int kAttendTcRows = 64;
+// A sequence with at least this many rows per kv head goes to the tensor-core
+// kernel, if the call's such sequences give the other one at least so many
+// steps (8 rows against 32 keys of 128 channels; it does about 780 a us).
+// Measured, register tiles / tensor cores, us: 8 x 4113 keys, 32 query and 8 kv
+// heads: 32 rows 57 / 64, 64 rows 97 / 66; one context of 32768: 55 / 60, 91 /
+// 60; 64 x 2048: 169 / 272, 324 / 273; but 16 x 1000 keys of 64 channels and 4
+// kv heads, 64 rows: 20 / 35 (16 thousand steps; the tensor-core kernel's
+// start and end take 25 us).
+constexpr int kAttendTcRows = 48;
+constexpr int kAttendTcSteps = 32768;
 
 inline void make_cache_ws_layout(const Geom& g, WsLayout* w) {
   make_ws_layout(g, w);

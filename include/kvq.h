@@ -358,6 +358,10 @@ typedef struct {
  * call may be replayed as appends advance them; out is then of the newest
  * tokens at that time.  The cache's contents must be finite (as the append's
  * are): an infinity or NaN in a key or value may reach rows that do not see it.
+ * A call runs on register tiles, on the tensor cores (many rows per kv head
+ * and many keys) or, sequence by sequence, on both.  The environment variable
+ * KVQ_ATTEND_TC, if set to 0 or 1, has the one or the other take every
+ * sequence (results stay within rounding of each other).
  * Errors (host side): KVQ_ERR_NULL, KVQ_ERR_ARG, KVQ_ERR_CAPACITY,
  * KVQ_ERR_EMPTY (n_q[b] > 0 on an empty sequence), KVQ_ERR_DTYPE,
  * KVQ_ERR_ALIGN, KVQ_ERR_BUFFER_TOO_SMALL; KVQ_ERR_CUDA on launch failure. */

@@ -25,7 +25,7 @@ def scores(q, k, n: int, scale: float, cap: float = 0.0, slopes=None, gqa: int =
     """[Hq, n_q, n] scores of q [n_q, Hq, d] against k [n, Hkv, d], before the mask."""
     n_q, hq, _ = q.shape
     kh = np.repeat(k.astype(np.float64), gqa, axis=1)
-    s = scale * np.einsum("ihd,jhd->hij", q.astype(np.float64), kh)
+    s = scale * np.matmul(q.astype(np.float64).transpose(1, 0, 2), kh.transpose(1, 2, 0))
     if cap:
         s = cap * np.tanh(s / cap)
     if slopes is not None:
@@ -80,11 +80,12 @@ def attend(cfg: o.Config, k16, v16, q, scale: float = 0.0, cap: float = 0.0, win
     tot = e.sum(-1, keepdims=True)
     alpha = np.divide(e, tot, out=np.zeros_like(e), where=tot > 0)
     v = np.repeat(vh.astype(np.float64), gqa, axis=1)
-    out = np.einsum("hij,jhd->ihd", alpha, v)
-    A = np.einsum("hij,jhd->ihd", alpha, np.abs(v))
+    v = v.transpose(1, 0, 2)
+    out = np.matmul(alpha, v).transpose(1, 0, 2)
+    A = np.matmul(alpha, np.abs(v)).transpose(1, 0, 2)
     # the dot product's mass: |q| (|s code| + |z|) <= |q| (|k| + 2 |z|), z at most the largest |k| of the channel
     kk = np.repeat(np.abs(kh).max(0)[None] * 3, gqa, axis=1)
-    mass = np.einsum("ihd,jhd->hij", np.abs(q), kk).max(-1).T                    # [n_q, Hq]
+    mass = (np.abs(q) * kk[0]).sum(-1)                                           # [n_q, Hq]
     big = np.where(seen & (alpha > 1e-9), np.abs(s), 0.0).max(-1).T + cap
     delta = scale * (2.0 ** -17 * mass + d * 15 * 2.0 ** -25) + 2.0 ** -20 * (1 + big)
     tol = 2.0 ** -11 * (np.abs(out) + 2 * A) + n * 2.0 ** -25 * np.abs(vh).max() + 2 * delta[..., None] * A + 2.0 ** -24

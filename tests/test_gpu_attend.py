@@ -11,6 +11,12 @@ from tests import kvq_testlib as tl
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(params=["registers", "tensor cores"], autouse=True)
+def kernel(request, monkeypatch):
+    """Every test runs with either kernel taking every sequence (the library's choice: test_the_librarys_choice)."""
+    monkeypatch.setenv("KVQ_ATTEND_TC", "1" if request.param == "tensor cores" else "0")
+
+
 def _hist(rng, lens, hkv, d):
     ks = [inputs.keys_channel_outliers(rng, n, hkv, d).astype(np.float16) for n in lens]
     vs = [(inputs.values_token_norms(rng, n, hkv, d) * 3 + 0.1).astype(np.float16) for n in lens]
@@ -158,6 +164,17 @@ def test_many_ragged_sequences():
     spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, len(lens), 96)
     ks, vs = _hist(rng, lens, hkv, d)
     _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, n_q, hkv * gqa, d, "fp16"), n_q)
+
+
+@pytest.mark.parametrize("lens,n_q", [([3000, 70, 900], [300, 1, 20]), ([2500] * 3, [64, 130, 1])])
+def test_the_librarys_choice(lens, n_q, monkeypatch):
+    """Sequences of one call on either kernel, by the rows and keys that they have."""
+    monkeypatch.delenv("KVQ_ATTEND_TC")
+    hkv, gqa, d = 8, 4, 128
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, 3, 3200)
+    rng = np.random.default_rng(len(lens) + n_q[0])
+    ks, vs = _hist(rng, lens, hkv, d)
+    _check(_filled(spec, ks, vs), spec, ks, vs, _queries(rng, n_q, hkv * gqa, d, "bf16"), n_q, "bf16", cap=50.0)
 
 
 def test_agrees_with_decode():

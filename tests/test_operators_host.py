@@ -62,11 +62,14 @@ def test_attend_plan(host, seed, dt):
     gqa = r.choice([1, 3, 4, 8])
     lens = [r.choice([1, 40, 1000, 4000]) for _ in range(seqs)]
     n_q = [r.choice([0, 1, 1, min(n, r.randint(1, 50)), n if n < 50 else 7, n]) for n in lens]
+    window = r.choice([0, 64])
     h = host.cache(lens, max_seqs=seqs, n_kv_heads=hkv, n_q_heads=hkv * gqa)
     host.log()
-    assert _attend(host, h, n_q=n_q, window=r.choice([0, 64]), dt=dt) == 0
+    assert _attend(host, h, n_q=n_q, window=window, dt=dt) == 0
     first = [sum(n_q[:b]) for b in range(seqs)]
     log, seen = host.log(), {}
+    keys = lambda b: min(lens[b], window + n_q[b]) if window else lens[b]  # noqa: E731
+    steps = sum(hkv * -(-n_q[b] * gqa // 8) * (keys(b) // 32 + 1) for b in range(seqs) if n_q[b] * gqa >= 48)
     while log:
         kind, n, seq0, split, pieces, unit, slot, residual = log[:8]
         assert kind == 1 and residual == (dt == 2) and unit in ((8, 128) if residual else (8, 256))
@@ -79,7 +82,7 @@ def test_attend_plan(host, seed, dt):
             rows, got = n_q[b] * gqa, offs[i + 1] - offs[i]
             if got == 0:
                 continue
-            assert b not in seen and (unit > 8) == (rows >= 64)
+            assert b not in seen and (unit > 8) == (rows >= 48 and steps >= 32768)
             seen[b] = True
             units = hkv * -(-rows // unit)
             assert got % units == 0 and got >= units
@@ -89,6 +92,16 @@ def test_attend_plan(host, seed, dt):
         assert cut == bool(split)
         assert not split or pieces * slot * (128 + 4) * 4 <= host.ws - 4 * 4096 - 512
     assert sorted(seen) == [b for b in range(seqs) if n_q[b]]
+
+
+@pytest.mark.parametrize("force", ["0", "1"])
+def test_attend_kernel_forced(host, force, monkeypatch):
+    monkeypatch.setenv("KVQ_ATTEND_TC", force)
+    h = host.cache([4000, 1, 300])
+    host.log()
+    assert _attend(host, h, n_q=[4000, 1, 7]) == 0
+    log = host.log()
+    assert log[5] == (256 if force == "1" else 8) and log[1] == 3 and len(log) == 8 + 9
 
 
 # ---------------------------------------------------------------- norm_rotary

@@ -13,11 +13,11 @@
 // row once (P fp64 products and as many sincospi) and every head of the row
 // uses them from registers.
 //
-// A lane owns 8 consecutive channels (one 16-byte load for 16-bit types), a
-// head row is D / 8 lanes, the norm is a butterfly over those lanes, and a
-// pair's partner comes from the lane P / 8 away.  Pairs split in the middle
-// of an 8-channel vector (P no multiple of 8, halves apart) take the partner
-// from shared memory instead.
+// A head row is D / 8 lanes.  A lane owns two pieces of 4 channels: the same
+// four of a pair's two halves (or 8 neighbours, where pairs are neighbours, or
+// behind the pairs), so that both members of a pair are in one lane; the norm
+// is a butterfly over the lanes.  Only pairs that split a piece (halves apart,
+// P no multiple of 4) take their partners from shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,47 +29,43 @@ namespace {
 
 constexpr int kRotThreads = 256;
 
-// Eight consecutive values as they are in memory, and as fp32.
+// A lane's two pieces of four values as they are in memory, and as fp32.
 template <int DT>
 struct Raw8 {
-  uint4 v[DT == KVQ_FP32 ? 2 : 1];
+  uint32_t v[DT == KVQ_FP32 ? 8 : 4];
 };
 template <int DT>
-__device__ __forceinline__ void load8(const void* base, int64_t idx, Raw8<DT>& r) {
-  const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(base) +
-                                                  idx * (DT == KVQ_FP32 ? 4 : 2));
-  r.v[0] = p[0];
-  if constexpr (DT == KVQ_FP32) r.v[1] = p[1];
+__device__ __forceinline__ void load8(const unsigned char* p0, const unsigned char* p1, Raw8<DT>& r) {
+  if constexpr (DT == KVQ_FP32) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p0), b = *reinterpret_cast<const uint4*>(p1);
+    r.v[0] = a.x; r.v[1] = a.y; r.v[2] = a.z; r.v[3] = a.w;
+    r.v[4] = b.x; r.v[5] = b.y; r.v[6] = b.z; r.v[7] = b.w;
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(p0), b = *reinterpret_cast<const uint2*>(p1);
+    r.v[0] = a.x; r.v[1] = a.y; r.v[2] = b.x; r.v[3] = b.y;
+  }
 }
 template <int DT>
 __device__ __forceinline__ void unpack8(const Raw8<DT>& r, float (&y)[8]) {
   if constexpr (DT == KVQ_FP32) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      y[4 * i] = __uint_as_float(r.v[i].x);
-      y[4 * i + 1] = __uint_as_float(r.v[i].y);
-      y[4 * i + 2] = __uint_as_float(r.v[i].z);
-      y[4 * i + 3] = __uint_as_float(r.v[i].w);
-    }
+    for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(r.v[i]);
   } else {
-    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = DT == KVQ_FP16
-                           ? __half22float2(*reinterpret_cast<const __half2*>(&w[i]))
-                           : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+                           ? __half22float2(*reinterpret_cast<const __half2*>(&r.v[i]))
+                           : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.v[i]));
       y[2 * i] = f.x;
       y[2 * i + 1] = f.y;
     }
   }
 }
-
 template <int DT>
-__device__ __forceinline__ void store8(void* base, int64_t idx, const float (&y)[8]) {
+__device__ __forceinline__ void store8(unsigned char* p0, unsigned char* p1, const float (&y)[8]) {
   if constexpr (DT == KVQ_FP32) {
-    float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + idx);
-    p[0] = make_float4(y[0], y[1], y[2], y[3]);
-    p[1] = make_float4(y[4], y[5], y[6], y[7]);
+    *reinterpret_cast<float4*>(p0) = make_float4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<float4*>(p1) = make_float4(y[4], y[5], y[6], y[7]);
   } else {
     uint32_t w[4];
 #pragma unroll
@@ -81,15 +77,21 @@ __device__ __forceinline__ void store8(void* base, int64_t idx, const float (&y)
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
     }
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + idx) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint2*>(p0) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(p1) = make_uint2(w[2], w[3]);
   }
+}
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float t = fmaf(-b, s, a * c);
+  b = fmaf(a, s, b * c);
+  a = t;
 }
 
 // Grid: x = rows, RB to a block; y = slices of the heads (a block takes the
 // passes slice, slice + gridDim.y, .. of kRotThreads / (D / 8) head rows).
 //
-// The block's rows share one round of angles, kept as factors of a channel and
-// of its partner (1 and 0 where nothing is rotated).  A thread keeps its head
+// The block's rows share one round of angles.  A thread keeps its head
 // through the RB rows (pointers step, the weight stays in registers) and has
 // the next pass's RB loads under way.  What bounds it then is the issue of
 // about 130 instructions for 32 x 8 values.
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kRotThreads, 3)
   constexpr int LPH = D / 8;                   // lanes of a head row
   constexpr int HPB = kRotThreads / LPH;       // head rows of one pass of the block
   constexpr int64_t IS = IN == KVQ_FP32 ? 4 : 2, OS = OUT == KVQ_FP32 ? 4 : 2;
-  __shared__ float4 cs[RB][D / 4], sn[RB][D / 4];
+  __shared__ float4 cs[RB][D / 8], sn[RB][D / 8];
   __shared__ float stage[kRotThreads * 8];
   const int tid = threadIdx.x, l = tid % LPH, hl = tid / LPH;
   const int b0 = blockIdx.x * RB;              // the block's first row, of the launch
@@ -107,11 +109,14 @@ __global__ void __launch_bounds__(kRotThreads, 3)
   const int P = a.n_pairs;
   const int nr = min(RB, rows - b0);
   const int heads = a.hq + a.hkv + (a.v ? a.hkv : 0);
-  const int e0 = 8 * l;                        // this lane's first channel
+  // this lane's pieces: channels o0 .. and o1 ..; of them pairs 4 l .. rotated
+  const bool apart = !a.interleaved && P % 4 == 0, staged = !a.interleaved && P % 4 != 0;
+  const int o0 = apart && 4 * l < P ? 4 * l : 8 * l, o1 = apart && 4 * l < P ? P + 4 * l : 8 * l + 4;
+  const int pairs = max(0, min(4, P - 4 * l));
 
   // this thread's head of the pass that starts at head h0
   struct Head {
-    const unsigned char* src;
+    const unsigned char* src;                  // its first row, at channel 0
     unsigned char* dst;
     int64_t src_step, dst_step;                // bytes between rows
     int part;                                  // 0 query, 1 key, 2 value, 3 none
@@ -127,28 +132,22 @@ __global__ void __launch_bounds__(kRotThreads, 3)
     h -= x.part == 0 ? 0 : x.part == 1 ? a.hq : a.hq + a.hkv;
     x.src_step = stride * IS;
     x.dst_step = wide * OS;
-    x.src = reinterpret_cast<const unsigned char*>(src) + row0 * x.src_step + (h * D + e0) * IS;
-    x.dst = reinterpret_cast<unsigned char*>(dst) + row0 * x.dst_step + (h * D + e0) * OS;
+    x.src = reinterpret_cast<const unsigned char*>(src) + row0 * x.src_step + h * D * IS;
+    x.dst = reinterpret_cast<unsigned char*>(dst) + row0 * x.dst_step + h * D * OS;
     return x;
   };
   auto load = [&](const Head& x, Raw8<IN> (&raw)[RB]) {
 #pragma unroll
     for (int r = 0; r < RB; ++r)
-      if (x.part < 3 && r < nr) load8<IN>(x.src + r * x.src_step, 0, raw[r]);
+      if (x.part < 3 && r < nr)
+        load8<IN>(x.src + r * x.src_step + o0 * IS, x.src + r * x.src_step + o1 * IS, raw[r]);
   };
   Raw8<IN> next[RB];
   Head ahead = head_of(blockIdx.y * HPB);
   load(ahead, next);
 
-  for (int i = tid; i < nr * (D / 2); i += kRotThreads) {
-    const int r = i / (D / 2), pair = i % (D / 2), line = b0 + r;
-    float* c = reinterpret_cast<float*>(cs[r]);
-    float* s = reinterpret_cast<float*>(sn[r]);
-    if (pair >= P) {                           // the channels behind the pairs
-      c[2 * pair] = c[2 * pair + 1] = 1.f;
-      s[2 * pair] = s[2 * pair + 1] = 0.f;
-      continue;
-    }
+  for (int i = tid; i < nr * P; i += kRotThreads) {
+    const int r = i / P, pair = i % P, line = b0 + r;
     int64_t pos;
     if (a.positions) {
       int axis = 0, end = a.sections[0];
@@ -165,21 +164,10 @@ __global__ void __launch_bounds__(kRotThreads, 3)
     }
     double t = (double)pos * (double)a.inv_freq[pair] * 0.15915494309189533577;   // 1 / (2 pi)
     t -= rint(t);
-    float sv, cv;
-    sincospif((float)(2.0 * t), &sv, &cv);
-    const int first = a.interleaved ? 2 * pair : pair, second = a.interleaved ? first + 1 : pair + P;
-    c[first] = c[second] = cv;
-    s[first] = -sv;
-    s[second] = sv;
+    sincospif((float)(2.0 * t), reinterpret_cast<float*>(sn[r]) + pair, reinterpret_cast<float*>(cs[r]) + pair);
   }
   __syncthreads();
 
-  // partners: in the lane, a lane P / 8 away, or (pairs that split a lane's
-  // eight channels) through shared memory
-  const bool in_lane = a.interleaved, shuffled = !in_lane && P % 8 == 0;
-  const int step = P / 8, from = l < step ? l + step : l < 2 * step ? l - step : l;
-  const int src_lane = (tid & 31) - l + from;
-  const int turned = 2 * P - e0;               // of this lane's channels, the first `turned` are rotated
   for (int h0 = blockIdx.y * HPB; h0 < heads; h0 += gridDim.y * HPB) {
     const Head x = ahead;
     Raw8<IN> raw[RB];
@@ -189,17 +177,16 @@ __global__ void __launch_bounds__(kRotThreads, 3)
       ahead = head_of(h0 + gridDim.y * HPB);
       load(ahead, next);
     }
-    const void* w = x.part == 0 ? a.q_weight : x.part == 1 ? a.k_weight : nullptr;
+    const unsigned char* w = reinterpret_cast<const unsigned char*>(
+        x.part == 0 ? a.q_weight : x.part == 1 ? a.k_weight : nullptr);
     float wv[8];
     if (w) {
       Raw8<IN> wr;
-      load8<IN>(w, e0, wr);
+      load8<IN>(w + o0 * IS, w + o1 * IS, wr);
       unpack8<IN>(wr, wv);
     }
-    const bool norm = __any_sync(0xffffffffu, w != nullptr), turn = __any_sync(0xffffffffu, x.part < 2);
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      if (r >= nr) break;
+    const bool norm = __any_sync(0xffffffffu, w != nullptr), line_up = staged && __any_sync(0xffffffffu, x.part < 2);
+    auto work = [&](int r) {
       float y[8];
       unpack8<IN>(raw[r], y);
       if (norm) {
@@ -214,41 +201,42 @@ __global__ void __launch_bounds__(kRotThreads, 3)
           for (int i = 0; i < 8; ++i) y[i] = y[i] * rms * wv[i];
         }
       }
-      if (turn) {
-        float z[8];
-        if (in_lane) {
+      if (line_up) {
+        float* row = stage + (tid - l) * 8;      // the head row, written and read by its own lanes
+        const float* c = reinterpret_cast<const float*>(cs[r]);
+        const float* s = reinterpret_cast<const float*>(sn[r]);
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = y[i ^ 1];
-        } else if (shuffled) {
+        for (int i = 0; i < 8; ++i) row[8 * l + i] = y[i];
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = __shfl_sync(0xffffffffu, y[i], src_lane);
-        } else {
-          float* line = stage + (tid - l) * 8;   // the head row, written and read by its own lanes
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) line[e0 + i] = y[i];
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
-            z[i] = e < P ? line[e + P] : e < 2 * P ? line[e - P] : 0.f;
-          }
+        for (int i = 0; i < 8; ++i) {
+          const int e = 8 * l + i;
+          if (x.part < 2 && e < P) y[i] = fmaf(-row[e + P], s[e], y[i] * c[e]);
+          else if (x.part < 2 && e < 2 * P) y[i] = fmaf(row[e - P], s[e - P], y[i] * c[e - P]);
         }
-        if (x.part < 2) {
-          const float4 c0 = cs[r][2 * l], c1 = cs[r][2 * l + 1], s0 = sn[r][2 * l], s1 = sn[r][2 * l + 1];
-          const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-          const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-          if (turned >= 8) {
+      } else if (x.part < 2 && pairs > 0) {
+        const float4 c4 = cs[r][l], s4 = sn[r][l];
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+        if (apart) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(z[i], s[i], y[i] * c[i]);
-          } else if (turned > 0) {
+          for (int i = 0; i < 4; ++i) turn(y[i], y[i + 4], c[i], s[i]);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < turned) y[i] = fmaf(z[i], s[i], y[i] * c[i]);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (i < pairs) turn(y[2 * i], y[2 * i + 1], c[i], s[i]);
         }
       }
-      if (x.part < 3) store8<OUT>(x.dst + r * x.dst_step, 0, y);
+      if (x.part < 3)
+        store8<OUT>(x.dst + r * x.dst_step + o0 * OS, x.dst + r * x.dst_step + o1 * OS, y);
+    };
+    if (nr == RB) {
+#pragma unroll
+      for (int r = 0; r < RB; ++r) work(r);
+    } else {
+#pragma unroll
+      for (int r = 0; r < RB; ++r)
+        if (r < nr) work(r);
     }
   }
 }

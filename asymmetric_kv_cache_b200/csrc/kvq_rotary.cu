@@ -88,26 +88,30 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = t;
 }
 
-// Grid: x = rows, RB to a block; y = slices of the heads (a block takes the
-// passes slice, slice + gridDim.y, .. of kRotThreads / (D / 8) head rows).
+// Grid: x = rows, NG groups of RB to a block; y = slices of the heads (a block
+// takes the passes slice, slice + gridDim.y, .. of kRotThreads / (D / 8) head
+// rows).
 //
-// The block's rows share one round of angles.  A thread keeps its head
-// through the RB rows (pointers step, the weight stays in registers) and has
-// the next pass's RB loads under way.  What bounds it then is the issue of
-// about 130 instructions for 32 x 8 values.
-template <int D, int IN, int OUT, int RB>
-__global__ void __launch_bounds__(kRotThreads, 3)
+// The block's rows share one round of angles.  A thread keeps its head through
+// RB rows (pointers step, the weight stays in registers) and has the next RB
+// loads under way.  16000 rows of 32 + 8 + 8 heads of 128, bf16 to fp16 (393
+// MB): one row to a block 158 us; four rows, the partner by shuffles, 119;
+// pairs in a lane 113; 8 rows to a block, two at a time, 64 registers and so
+// four blocks on an SM, 109 (92 without the norms): 3.6 TB/s, 0.55 of the
+// measured copy, at about 120 instructions for 32 x 8 values.
+template <int D, int IN, int OUT, int RB, int NG>
+__global__ void __launch_bounds__(kRotThreads, 4)
     norm_rotary_kernel(const RotaryArgs a, const RotarySeqs seqs, int rows) {
   constexpr int LPH = D / 8;                   // lanes of a head row
   constexpr int HPB = kRotThreads / LPH;       // head rows of one pass of the block
   constexpr int64_t IS = IN == KVQ_FP32 ? 4 : 2, OS = OUT == KVQ_FP32 ? 4 : 2;
-  __shared__ float4 cs[RB][D / 8], sn[RB][D / 8];
+  __shared__ float4 cs[RB * NG][D / 8], sn[RB * NG][D / 8];
   __shared__ float stage[kRotThreads * 8];
   const int tid = threadIdx.x, l = tid % LPH, hl = tid / LPH;
-  const int b0 = blockIdx.x * RB;              // the block's first row, of the launch
+  const int b0 = blockIdx.x * (RB * NG);       // the block's first row, of the launch
   const int64_t row0 = seqs.row0 + b0;
   const int P = a.n_pairs;
-  const int nr = min(RB, rows - b0);
+  const int all = min(RB * NG, rows - b0);
   const int heads = a.hq + a.hkv + (a.v ? a.hkv : 0);
   // this lane's pieces: channels o0 .. and o1 ..; of them pairs 4 l .. rotated
   const bool apart = !a.interleaved && P % 4 == 0, staged = !a.interleaved && P % 4 != 0;
@@ -136,17 +140,18 @@ __global__ void __launch_bounds__(kRotThreads, 3)
     x.dst = reinterpret_cast<unsigned char*>(dst) + row0 * x.dst_step + h * D * OS;
     return x;
   };
-  auto load = [&](const Head& x, Raw8<IN> (&raw)[RB]) {
+  auto load = [&](const Head& x, int g0, Raw8<IN> (&raw)[RB]) {
 #pragma unroll
     for (int r = 0; r < RB; ++r)
-      if (x.part < 3 && r < nr)
-        load8<IN>(x.src + r * x.src_step + o0 * IS, x.src + r * x.src_step + o1 * IS, raw[r]);
+      if (x.part < 3 && g0 + r < all)
+        load8<IN>(x.src + (g0 + r) * x.src_step + o0 * IS, x.src + (g0 + r) * x.src_step + o1 * IS, raw[r]);
   };
   Raw8<IN> next[RB];
   Head ahead = head_of(blockIdx.y * HPB);
-  load(ahead, next);
+  int gn = 0, hn = blockIdx.y * HPB;           // group's first row and first head of the loads under way
+  load(ahead, gn, next);
 
-  for (int i = tid; i < nr * P; i += kRotThreads) {
+  for (int i = tid; i < all * P; i += kRotThreads) {
     const int r = i / P, pair = i % P, line = b0 + r;
     int64_t pos;
     if (a.positions) {
@@ -168,14 +173,20 @@ __global__ void __launch_bounds__(kRotThreads, 3)
   }
   __syncthreads();
 
-  for (int h0 = blockIdx.y * HPB; h0 < heads; h0 += gridDim.y * HPB) {
+  while (gn < all) {
     const Head x = ahead;
+    const int g0 = gn, nr = min(RB, all - g0);
     Raw8<IN> raw[RB];
 #pragma unroll
     for (int r = 0; r < RB; ++r) raw[r] = next[r];
-    if (h0 + (int)gridDim.y * HPB < heads) {
-      ahead = head_of(h0 + gridDim.y * HPB);
-      load(ahead, next);
+    hn += gridDim.y * HPB;
+    if (hn >= heads) {
+      hn = blockIdx.y * HPB;
+      gn += RB;
+    }
+    if (gn < all) {
+      ahead = head_of(hn);
+      load(ahead, gn, next);
     }
     const unsigned char* w = reinterpret_cast<const unsigned char*>(
         x.part == 0 ? a.q_weight : x.part == 1 ? a.k_weight : nullptr);
@@ -203,8 +214,8 @@ __global__ void __launch_bounds__(kRotThreads, 3)
       }
       if (line_up) {
         float* row = stage + (tid - l) * 8;      // the head row, written and read by its own lanes
-        const float* c = reinterpret_cast<const float*>(cs[r]);
-        const float* s = reinterpret_cast<const float*>(sn[r]);
+        const float* c = reinterpret_cast<const float*>(cs[g0 + r]);
+        const float* s = reinterpret_cast<const float*>(sn[g0 + r]);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) row[8 * l + i] = y[i];
@@ -216,7 +227,7 @@ __global__ void __launch_bounds__(kRotThreads, 3)
           else if (x.part < 2 && e < 2 * P) y[i] = fmaf(row[e - P], s[e - P], y[i] * c[e - P]);
         }
       } else if (x.part < 2 && pairs > 0) {
-        const float4 c4 = cs[r][l], s4 = sn[r][l];
+        const float4 c4 = cs[g0 + r][l], s4 = sn[g0 + r][l];
         const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
         if (apart) {
 #pragma unroll
@@ -228,7 +239,7 @@ __global__ void __launch_bounds__(kRotThreads, 3)
         }
       }
       if (x.part < 3)
-        store8<OUT>(x.dst + r * x.dst_step + o0 * OS, x.dst + r * x.dst_step + o1 * OS, y);
+        store8<OUT>(x.dst + (g0 + r) * x.dst_step + o0 * OS, x.dst + (g0 + r) * x.dst_step + o1 * OS, y);
     };
     if (nr == RB) {
 #pragma unroll
@@ -254,12 +265,11 @@ cudaError_t launch_norm_rotary(int d, int dtype, int out_dtype, const RotaryArgs
 #define KVQ_ROTARY_CASE(D_, I_, O_)                                                       \
   if (d == D_ && dtype == I_ && out_dtype == O_) {                                        \
     if (few)                                                                              \
-      norm_rotary_kernel<D_, I_, O_, 1><<<dim3((unsigned)rows, (unsigned)slices),         \
-                                          kRotThreads, 0, stream>>>(a, seqs, rows);       \
+      norm_rotary_kernel<D_, I_, O_, 1, 1><<<dim3((unsigned)rows, (unsigned)slices),      \
+                                             kRotThreads, 0, stream>>>(a, seqs, rows);    \
     else                                                                                  \
-      norm_rotary_kernel<D_, I_, O_, I_ == KVQ_FP32 ? 2 : 4>                              \
-          <<<(unsigned)((rows + (I_ == KVQ_FP32 ? 1 : 3)) / (I_ == KVQ_FP32 ? 2 : 4)),    \
-             kRotThreads, 0, stream>>>(a, seqs, rows);                                    \
+      norm_rotary_kernel<D_, I_, O_, 2, 4><<<(unsigned)((rows + 7) / 8), kRotThreads, 0,  \
+                                             stream>>>(a, seqs, rows);                    \
     return cudaGetLastError();                                                            \
   }
 #define KVQ_ROTARY_OUT(D_, I_) \

@@ -10,8 +10,8 @@
 //     as an fp16 value K1 and the fp16 residual K2 of the exact number (the
 //     product's by a fused multiply-subtract, the sum's by the error-free
 //     two-sum), v = s code + z rounded to fp16 once.  The codes' storage
-//     order is the order of the operand's 8 x 16-byte core matrices, a lane's
-//     pair per core row, so every 32-lane store is one core matrix.
+//     order is that of 8 x 8 matrix fragments, and an operand's core matrices
+//     are 8 rows of 16 bytes: one matrix store writes four of them.
 //   * S = Q K1^T + Q K2^T (Q as A operand in tensor memory: from shared memory
 //     it would take the bandwidth that K needs, 128 + 64 bytes a cycle of
 //     128) and O += P V (P from shared memory, so that the next S may follow
@@ -185,6 +185,16 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
+// Four 8 x 8 matrices of 16-bit elements held a row pair per lane (lane 4 r +
+// i: row r, columns 2 i and 2 i + 1), each to 8 rows of 16 bytes: lane l gives
+// the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                          uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 // Operands of 16 tokens (16-token part `sub` of the 32 tokens hf of a block in
 // shared memory): token eights te, te + 1 of the tile.  `wait` is called between the loads
 // and the stores.
@@ -208,28 +218,38 @@ __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, 
   lds_words<2 * J>(word(OFF_VS + (4 * kv + i4) * J * 8), vs);
   lds_words<2 * J>(word(OFF_VZ + (4 * kv + i4) * J * 8), vz);
   wait();
-  unsigned char* k1 = stage + te * P * 128 + lane * 4;
-  unsigned char* v1 = stage + 2 * TcAtt<D>::K_BYTES + te * 128 + lane * 4;
-  static_for<P>([&](auto pc) {
-    constexpr int p = decltype(pc)::value;
+  // this lane's row of its matrix of four: neighbouring channel eights for the
+  // keys, (channel eight, token eight) for the values
+  const uint32_t k1 = smem_u32(stage) + (te * P + lane / 8) * 128 + lane % 8 * 16;
+  const uint32_t v1 = smem_u32(stage) + 2 * TcAtt<D>::K_BYTES +
+                      ((lane / 8 & 1) * (kTcKeys / 8) + te + lane / 16) * 128 + lane % 8 * 16;
+  static_for<P / 4>([&](auto pc) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const uint32_t c = unpack_pair<KBL, p % FK>(kw[x][p / FK]);
-      const uint32_t h = hmul2_b(c, ks[p]), e = hfma2_negc_b(c, ks[p], h);   // c s = h + e
-      const uint32_t hi = hadd2_b(h, kz[p]), b = hsub2_b(hi, h);             // h + z = hi + f
-      const uint32_t f = hadd2_b(hsub2_b(h, hsub2_b(hi, b)), hsub2_b(kz[p], b));
-      *reinterpret_cast<uint32_t*>(k1 + (x * P + p) * 128) = hi;
-      *reinterpret_cast<uint32_t*>(k1 + TcAtt<D>::K_BYTES + (x * P + p) * 128) = hadd2_b(e, f);
+      uint32_t hi[4], lo[4];
+      static_for<4>([&](auto qc) {
+        constexpr int q = decltype(qc)::value, p = 4 * decltype(pc)::value + q;
+        const uint32_t c = unpack_pair<KBL, p % FK>(kw[x][p / FK]);
+        const uint32_t h = hmul2_b(c, ks[p]), e = hfma2_negc_b(c, ks[p], h);   // c s = h + e
+        hi[q] = hadd2_b(h, kz[p]);                                             // h + z = hi + f
+        const uint32_t b = hsub2_b(hi[q], h);
+        const uint32_t f = hadd2_b(hsub2_b(h, hsub2_b(hi[q], b)), hsub2_b(kz[p], b));
+        lo[q] = hadd2_b(e, f);
+      });
+      const uint32_t at = k1 + (x * P + 4 * decltype(pc)::value) * 128;
+      stmatrix4(at, hi[0], hi[1], hi[2], hi[3]);
+      stmatrix4(at + TcAtt<D>::K_BYTES, lo[0], lo[1], lo[2], lo[3]);
     }
   });
   static_for<MT>([&](auto mc) {
     constexpr int mt = decltype(mc)::value;
     constexpr int j = 16 * mt / G, w = mt / (FV / 4), u = mt % (FV / 4);
+    uint32_t o[4];
     static_for<4>([&](auto qc) {
-      constexpr int hr = decltype(qc)::value & 1, kh = decltype(qc)::value >> 1;
-      *reinterpret_cast<uint32_t*>(v1 + ((2 * mt + hr) * (kTcKeys / 8) + kh) * 128) = hfma2_b(
-          unpack_pair<VB, 2 * u + hr + FV / 2 * kh>(vw[w]), vs[2 * j + kh], vz[2 * j + kh]);
+      constexpr int q = decltype(qc)::value, hr = q & 1, kh = q >> 1;
+      o[q] = hfma2_b(unpack_pair<VB, 2 * u + hr + FV / 2 * kh>(vw[w]), vs[2 * j + kh], vz[2 * j + kh]);
     });
+    stmatrix4(v1 + 2 * mt * (kTcKeys / 8) * 128, o[0], o[1], o[2], o[3]);
   });
 }
 

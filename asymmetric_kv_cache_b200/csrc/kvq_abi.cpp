@@ -431,6 +431,10 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   if (!std::isfinite(sc.scale) || sc.scale < 0.f || !std::isfinite(sc.cap) || sc.cap < 0.f)
     return fail(KVQ_ERR_ARG, "scale and cap must be finite and >= 0 (got %g, %g)", sc.scale, sc.cap);
   if (sc.window < 0) return fail(KVQ_ERR_ARG, "window %d < 0", sc.window);
+  const float scale = sc.scale > 0.f ? sc.scale : 1.0f / std::sqrt((float)g.d);
+  if (!std::isfinite(scale * 1.5f) || !std::isfinite(sc.cap * 3.f) ||
+      (sc.cap > 0.f && !std::isfinite(scale / sc.cap * 3.f)))
+    return fail(KVQ_ERR_ARG, "scale %g and cap %g leave fp32's range", scale, sc.cap);
   if (!aligned(sc.slopes, 4) || !aligned(sc.prefix, 4))
     return fail(KVQ_ERR_ALIGN, "slopes and prefix must be 4-byte aligned");
   int64_t total = 0;
@@ -464,7 +468,7 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   a.q_dtype = q_dtype;
   a.out = out;
   a.ws = static_cast<unsigned char*>(workspace);
-  a.scale = sc.scale > 0.f ? sc.scale : 1.0f / std::sqrt((float)g.d);
+  a.scale = scale;
   a.cap = sc.cap;
   a.score_window = sc.window;
   a.slopes = sc.slopes;
@@ -623,7 +627,15 @@ kvq_status kvq_reorder(kvq_cache* cache, const int32_t* parent, int32_t n_seq,
       return fail(KVQ_ERR_ARG, "sequences %d and %d cannot share %d tokens (they hold %d and %d)", b,
                   parent[b], shared_tokens, cache->lens[b], cache->lens[parent[b]]);
   }
-  const std::vector<kvq::ReorderMove> all = kvq::plan_reorder(parent, n_seq, cache->cfg.max_seqs);
+  std::vector<kvq::ReorderMove> all;
+  std::vector<int32_t> after;
+  try {
+    all = kvq::plan_reorder(parent, n_seq, cache->cfg.max_seqs);
+    after = cache->lens;
+  } catch (const std::bad_alloc&) {
+    return fail(KVQ_ERR_ARG, "out of host memory");
+  }
+  for (int b = 0; b < n_seq; ++b) after[b] = cache->lens[parent[b]];
   static thread_local kvq::ReorderMoves mv;
   for (size_t at = 0; at < all.size();) {
     const size_t from = at;
@@ -637,8 +649,7 @@ kvq_status kvq_reorder(kvq_cache* cache, const int32_t* parent, int32_t n_seq,
     cudaError_t e = kvq::launch_reorder(g, cache->buf, mv, shared_tokens, bytes, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "reorder launch");
   }
-  std::vector<int32_t> old(cache->lens);
-  for (int b = 0; b < n_seq; ++b) cache->lens[b] = old[parent[b]];
+  cache->lens.swap(after);
   return ok();
 }
 

@@ -43,10 +43,10 @@ static_assert(2 * kTcRegsSoftmax + 2 * kTcRegsOperands + kTcRegsRest <= 5 * kTcR
               "the groups' registers come out of the launch's");
 constexpr float kTcSlack = 8.f;           // a maximum may be passed by 2^8 before O is rescaled
 
-template <int D>
+template <int D, int KB, int VB, int G>
 struct TcAtt {
-  // blocks on their way: 64 tokens of the largest blocks (K4 / V4: 40 D bytes a 32)
-  static constexpr int RAW = 80 * D, NRAW = 3;
+  // blocks on their way: 64 tokens
+  static constexpr int RAW = 64 / G * AttCfg<D, KB, VB, G>::BLK;
   static constexpr int K_BYTES = kTcKeys * D * 2;        // K1, K2, V each
   static constexpr int STAGE = 3 * K_BYTES;
   static constexpr int NST = 3;                          // (the barriers of the tiles rely on it)
@@ -56,12 +56,20 @@ struct TcAtt {
   static constexpr int IO_ROW = 4 * D + 16;
   static constexpr int IO_BYTES = 8 * 32 * IO_ROW;
   static constexpr int AREA = NST * STAGE > IO_BYTES ? NST * STAGE : IO_BYTES;
+  // two P areas for each row tile where they fit: a weight tile is then written
+  // without a wait, as S of its key tile says (its commit came after it) that
+  // the product two tiles before has read its area.  Else the product one tile
+  // before is waited for.
+  static constexpr int NP = AREA + 4 * P_BYTES + 2 * RAW + 128 <= 227 * 1024 ? 2 : 1;
+  static constexpr int NRAW = AREA + 2 * NP * P_BYTES + 3 * RAW + 128 <= 227 * 1024 ? 3 : 2;
   static constexpr int P_OFF = AREA;
-  static constexpr int RAW_OFF = P_OFF + 2 * P_BYTES;
+  static constexpr int RAW_OFF = P_OFF + 2 * NP * P_BYTES;
   static constexpr int BAR = RAW_OFF + NRAW * RAW;
   // mbarriers: empty[NST], s_full[2], pv_done[2], raw_full[NRAW], raw_empty[NRAW]
   static constexpr int B_EMPTY = 0, B_S = NST, B_PV = B_S + 2, B_RF = B_PV + 2, B_RE = B_RF + NRAW, NBAR = B_RE + NRAW;
-  static constexpr int SMEM = BAR + NBAR * 8;
+  static constexpr int TM = BAR + NBAR * 8;               // the tensor memory's address
+  static constexpr int SMEM = TM + 8;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
   // tensor memory columns
   static constexpr uint32_t T_S = 0, T_Q = 128, T_O = 128 + D, T_COLS = 512;
   static_assert(T_O + 2 * D <= T_COLS, "tensor memory");
@@ -148,12 +156,15 @@ __host__ __device__ constexpr uint32_t att_tc_idesc(int n) {
 // barrier 274).  So of the operand warps, which wait most of the time, one
 // polls for its team and the others wait at a hardware barrier, which costs
 // nothing; and hand-offs to the issuing warp (S read, P written, operands
-// written) are hardware barriers: the giving side arrives, that warp syncs.  Every barrier's next use waits, by
-// the data flow, for the issuing warp to have passed this one.
+// written) are hardware barriers: the giving side arrives, that warp syncs.  Every
+// barrier's next use waits, by the data flow, for the issuing warp to have
+// passed this one (S of tile t + 1 is issued after the barrier of S read of
+// tile t, and before that of P of tile t: P's alternate between two).
 // A polled wait is bounded; one that runs out is recorded, later ones of the
 // warp are skipped, and the roles run on to their ends over whatever the
 // buffers hold, so that all meet at every hardware barrier.
-enum { kBarOp0 = 1, kBarOp1, kBarSrA, kBarSrB, kBarPA, kBarPB, kBarFull0, kBarFull1 };
+enum { kBarOp0 = 1, kBarOp1, kBarSrA, kBarSrB, kBarPA, kBarPB, kBarPA1, kBarPB1,
+       kBarFull0, kBarFull1 };
 __device__ __forceinline__ void att_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -162,11 +173,11 @@ __device__ __forceinline__ void att_bar_arrive(int id, int threads) {
 }
 __device__ __forceinline__ void att_tc_wait(uint64_t* bar, uint32_t parity, bool& ok, int32_t* err,
                                             int lane) {
-  if (!ok) return;
-  if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity))) {
+  if (ok && !mbar_wait_bounded(bar, parity)) {
     ok = false;
     if (lane == 0) atomicExch(err, KVQ_ERR_DEVICE);
   }
+  __syncwarp();
 }
 
 __device__ __forceinline__ uint32_t hadd2_b(uint32_t a, uint32_t b) {
@@ -221,7 +232,7 @@ __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, 
   // this lane's row of its matrix of four: neighbouring channel eights for the
   // keys, (channel eight, token eight) for the values
   const uint32_t k1 = smem_u32(stage) + (te * P + lane / 8) * 128 + lane % 8 * 16;
-  const uint32_t v1 = smem_u32(stage) + 2 * TcAtt<D>::K_BYTES +
+  const uint32_t v1 = smem_u32(stage) + 2 * (kTcKeys * D * 2) +
                       ((lane / 8 & 1) * (kTcKeys / 8) + te + lane / 16) * 128 + lane % 8 * 16;
   static_for<P / 4>([&](auto pc) {
 #pragma unroll
@@ -238,7 +249,7 @@ __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, 
       });
       const uint32_t at = k1 + (x * P + 4 * decltype(pc)::value) * 128;
       stmatrix4(at, hi[0], hi[1], hi[2], hi[3]);
-      stmatrix4(at + TcAtt<D>::K_BYTES, lo[0], lo[1], lo[2], lo[3]);
+      stmatrix4(at + (kTcKeys * D * 2), lo[0], lo[1], lo[2], lo[3]);
     }
   });
   static_for<MT>([&](auto mc) {
@@ -265,7 +276,7 @@ __device__ __forceinline__ void tc_fill_fp16(const __half* k, const __half* v, i
   const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
   wait();
   unsigned char* k1 = stage + te * P * 128 + lane * 4;
-  unsigned char* v1 = stage + 2 * TcAtt<D>::K_BYTES + te * 128 + lane * 4;
+  unsigned char* v1 = stage + 2 * (kTcKeys * D * 2) + te * 128 + lane * 4;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const bool there = 8 * x + g8 < valid;
@@ -273,7 +284,7 @@ __device__ __forceinline__ void tc_fill_fp16(const __half* k, const __half* v, i
     for (int p = 0; p < P; ++p) {
       *reinterpret_cast<uint32_t*>(k1 + (x * P + p) * 128) =
           there ? kw[(8 * x + g8) * (D / 2) + 4 * p + i4] : 0u;
-      *reinterpret_cast<uint32_t*>(k1 + TcAtt<D>::K_BYTES + (x * P + p) * 128) = 0u;
+      *reinterpret_cast<uint32_t*>(k1 + (kTcKeys * D * 2) + (x * P + p) * 128) = 0u;
     }
   }
 #pragma unroll
@@ -314,11 +325,11 @@ struct TcKeys {
 template <int D, int KB, int VB, int G>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attend_tc_kernel(const Geom g, const WsLayout w, const AttendArgs a, const AttendSeqs seqs) {
-  using C = TcAtt<D>;
+  using C = TcAtt<D, KB, VB, G>;
   extern __shared__ __align__(1024) unsigned char att_tc_smem[];
   unsigned char* const smem = att_tc_smem;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR);
-  __shared__ uint32_t tmem_base;
+  uint32_t& tmem_base = *reinterpret_cast<uint32_t*>(smem + C::TM);
   // (the shuffles tell the compiler that these are the same in all lanes: the
   // products' operands then stay in uniform registers)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -471,7 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int c_hi = min(nb, c_b + (w_lo - 31 >= pos_b ? (w_lo - 31 - pos_b) / 32 + 1 : 0));
       const bool plain = a.cap == 0.f && !a.slopes;
       // this row of P: core matrices of 8 rows x 8 keys, a row eight 1024 bytes
-      unsigned char* prow = smem + C::P_OFF + X * C::P_BYTES + ((wrow & 127) + lane) / 8 * 1024 + lane % 8 * 16;
+      unsigned char* prow = smem + C::P_OFF + X * C::NP * C::P_BYTES + ((wrow & 127) + lane) / 8 * 1024 + lane % 8 * 16;
       float m = -INFINITY, l = 0.f;
       const uint32_t ts = tm + lanes + C::T_S + kTcKeys * X, to = tm + lanes + C::T_O + D * X;
       for (int t = 0; t < nt; ++t) {
@@ -562,14 +573,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           upk2(add2(sum[0], sum[1]), x, y);
           l += x + y;
         }
-        // the product before this one has read P
-        if (t > 0) att_tc_wait(&bars[C::B_PV + X], (t - 1) & 1, ok, err, lane);
+        unsigned char* const pt = prow + (C::NP == 2 && t & 1 ? C::P_BYTES : 0);
+        if (C::NP == 1 && t > 0) att_tc_wait(&bars[C::B_PV + X], (t - 1) & 1, ok, err, lane);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(prow + 128 * i) =
+          *reinterpret_cast<uint4*>(pt + 128 * i) =
               make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
         fence_proxy_async_smem();
-        att_bar_arrive(kBarPA + X, 160);
+        att_bar_arrive(kBarPA + X + 2 * (t & 1), 160);
       }
       // ---- the result, through the stages: once both tiles' last products are
       // done (the last key tile's stage is free: nobody waits for later phases)
@@ -637,7 +648,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       att_bar_sync(kBarOp0 + team, 128);
       if (c < keys.nblk * keys.per) {
         const int grp = keys.group(c);
-        const unsigned char* blk = smem + C::RAW_OFF + (t % C::NRAW) * C::RAW + (G == 32 ? c2 * C::RAW / 2 : 0);
+        const unsigned char* blk = smem + C::RAW_OFF + (t % C::NRAW) * C::RAW + (G == 32 ? c2 * (C::RAW / 2) : 0);
         bool narrow = false;
         if constexpr (KB == 4) {
           narrow = g.akvq_delta && akvq_key_bits(grp, n, G, g.akvq_delta) == 2;
@@ -668,7 +679,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int x = warp - 16;
     const uint32_t sb = smem_u32(smem);
     const uint32_t d_s = tm + C::T_S + kTcKeys * x, d_o = tm + C::T_O + D * x, q = tm + C::T_Q + (D / 2) * x;
-    const uint64_t dp = att_tc_desc(sb + C::P_OFF + C::P_BYTES * x, kTcKeys * 16);
     for (int t = -1; t < nt; ++t) {
       if (t + 1 < nt) {
         const uint32_t stage = sb + (t + 1) % C::NST * C::STAGE;
@@ -691,7 +701,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (t < 0) continue;
       const uint64_t dv = att_tc_desc(sb + t % C::NST * C::STAGE + 2 * C::K_BYTES, kTcKeys * 16);
-      att_bar_sync(kBarPA + x, 160);
+      const uint64_t dp = att_tc_desc(sb + C::P_OFF + C::P_BYTES * (C::NP * x + (C::NP == 2 ? t & 1 : 0)), kTcKeys * 16);
+      att_bar_sync(kBarPA + x + 2 * (t & 1), 160);
       att_tc_fence_after();
       if (att_elect()) {
 #pragma unroll
@@ -775,7 +786,7 @@ cudaError_t launch_attend_tc_t(const Geom& g, const WsLayout& w, const AttendArg
   if (e != cudaSuccess) return e;
   if (!(ready.load() >> (dev & 63) & 1)) {
     e = cudaFuncSetAttribute(attend_tc_kernel<D, KB, VB, G>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, TcAtt<D>::SMEM);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, TcAtt<D, KB, VB, G>::SMEM);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, attend_tc_kernel<D, KB, VB, G>);
@@ -783,7 +794,7 @@ cudaError_t launch_attend_tc_t(const Geom& g, const WsLayout& w, const AttendArg
     if (fa.numRegs < kTcRegs) return cudaErrorInvalidKernelImage;
     ready.fetch_or(1ull << (dev & 63));
   }
-  return attend_launch(attend_tc_kernel<D, KB, VB, G>, s.piece_off[s.n], kTcThreads, TcAtt<D>::SMEM, stream, g, w,
+  return attend_launch(attend_tc_kernel<D, KB, VB, G>, s.piece_off[s.n], kTcThreads, TcAtt<D, KB, VB, G>::SMEM, stream, g, w,
                        a, s);
 }
 

@@ -41,6 +41,7 @@ def test_attend_refusals(host):
         (dict(n_q=[1], ws_bytes=host.ws - 1), H.SMALL), (dict(n_q=[1], scale=-1.0), H.ARG),
         (dict(n_q=[1], scale=float("nan")), H.ARG), (dict(n_q=[1], cap=-2.0), H.ARG),
         (dict(n_q=[1], cap=float("inf")), H.ARG), (dict(n_q=[1], window=-1), H.ARG),
+        (dict(n_q=[1], scale=3e38), H.ARG), (dict(n_q=[1], cap=2e38), H.ARG), (dict(n_q=[1], scale=1.0, cap=1e-39), H.ARG),
     ]
     for kw, want in cases:
         assert _attend(host, h, **kw) == want, kw

@@ -93,12 +93,14 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 // rows).
 //
 // The block's rows share one round of angles.  A thread keeps its head through
-// RB rows (pointers step, the weight stays in registers) and has the next RB
+// them (pointers step, the weight stays in registers) and has the next RB
 // loads under way.  16000 rows of 32 + 8 + 8 heads of 128, bf16 to fp16 (393
-// MB): one row to a block 158 us; four rows, the partner by shuffles, 119;
-// pairs in a lane 113; 8 rows to a block, two at a time, 64 registers and so
-// four blocks on an SM, 109 (92 without the norms): 3.6 TB/s, 0.55 of the
-// measured copy, at about 120 instructions for 32 x 8 values.
+// MB), us: one row to a block 158; four, the partner by shuffles, 119; pairs in
+// a lane 113; 8 rows to a block, two at a time, in 64 registers and so four
+// blocks on an SM, 109; a head through all 8 rows 103 (94 without the norms):
+// 3.8 TB/s, 0.58 of the measured copy.  Issue and the loads' latency bound it
+// together; prefetching the block's rows into the second-level cache made it
+// 119.
 template <int D, int IN, int OUT, int RB, int NG>
 __global__ void __launch_bounds__(kRotThreads, 4)
     norm_rotary_kernel(const RotaryArgs a, const RotarySeqs seqs, int rows) {
@@ -148,8 +150,7 @@ __global__ void __launch_bounds__(kRotThreads, 4)
   };
   Raw8<IN> next[RB];
   Head ahead = head_of(blockIdx.y * HPB);
-  int gn = 0, hn = blockIdx.y * HPB;           // group's first row and first head of the loads under way
-  load(ahead, gn, next);
+  load(ahead, 0, next);
 
   for (int i = tid; i < all * P; i += kRotThreads) {
     const int r = i / P, pair = i % P, line = b0 + r;
@@ -173,21 +174,8 @@ __global__ void __launch_bounds__(kRotThreads, 4)
   }
   __syncthreads();
 
-  while (gn < all) {
+  for (int h0 = blockIdx.y * HPB; h0 < heads; h0 += gridDim.y * HPB) {
     const Head x = ahead;
-    const int g0 = gn, nr = min(RB, all - g0);
-    Raw8<IN> raw[RB];
-#pragma unroll
-    for (int r = 0; r < RB; ++r) raw[r] = next[r];
-    hn += gridDim.y * HPB;
-    if (hn >= heads) {
-      hn = blockIdx.y * HPB;
-      gn += RB;
-    }
-    if (gn < all) {
-      ahead = head_of(hn);
-      load(ahead, gn, next);
-    }
     const unsigned char* w = reinterpret_cast<const unsigned char*>(
         x.part == 0 ? a.q_weight : x.part == 1 ? a.k_weight : nullptr);
     float wv[8];
@@ -197,57 +185,70 @@ __global__ void __launch_bounds__(kRotThreads, 4)
       unpack8<IN>(wr, wv);
     }
     const bool norm = __any_sync(0xffffffffu, w != nullptr), line_up = staged && __any_sync(0xffffffffu, x.part < 2);
-    auto work = [&](int r) {
-      float y[8];
-      unpack8<IN>(raw[r], y);
-      if (norm) {
-        float ss = 0.f;
+#pragma unroll 1
+    for (int g0 = 0; g0 < all; g0 += RB) {
+      const int nr = min(RB, all - g0);
+      Raw8<IN> raw[RB];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w) {
-          const float rms = rsqrtf(ss * (1.0f / D) + a.eps);   // off by 2^-22 at most
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = y[i] * rms * wv[i];
-        }
+      for (int r = 0; r < RB; ++r) raw[r] = next[r];
+      if (g0 + RB < all) {
+        load(x, g0 + RB, next);
+      } else if (h0 + (int)gridDim.y * HPB < heads) {
+        ahead = head_of(h0 + gridDim.y * HPB);
+        load(ahead, 0, next);
       }
-      if (line_up) {
-        float* row = stage + (tid - l) * 8;      // the head row, written and read by its own lanes
-        const float* c = reinterpret_cast<const float*>(cs[g0 + r]);
-        const float* s = reinterpret_cast<const float*>(sn[g0 + r]);
-        __syncwarp();
+      auto work = [&](int r) {
+        float y[8];
+        unpack8<IN>(raw[r], y);
+        if (norm) {
+          float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) row[8 * l + i] = y[i];
-        __syncwarp();
+          for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = 8 * l + i;
-          if (x.part < 2 && e < P) y[i] = fmaf(-row[e + P], s[e], y[i] * c[e]);
-          else if (x.part < 2 && e < 2 * P) y[i] = fmaf(row[e - P], s[e - P], y[i] * c[e - P]);
+          for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (w) {
+            const float rms = rsqrtf(ss * (1.0f / D) + a.eps);   // off by 2^-22 at most
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = y[i] * rms * wv[i];
+          }
         }
-      } else if (x.part < 2 && pairs > 0) {
-        const float4 c4 = cs[g0 + r][l], s4 = sn[g0 + r][l];
-        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-        if (apart) {
+        if (line_up) {
+          float* row = stage + (tid - l) * 8;      // the head row, written and read by its own lanes
+          const float* c = reinterpret_cast<const float*>(cs[g0 + r]);
+          const float* s = reinterpret_cast<const float*>(sn[g0 + r]);
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) turn(y[i], y[i + 4], c[i], s[i]);
-        } else {
+          for (int i = 0; i < 8; ++i) row[8 * l + i] = y[i];
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < pairs) turn(y[2 * i], y[2 * i + 1], c[i], s[i]);
+          for (int i = 0; i < 8; ++i) {
+            const int e = 8 * l + i;
+            if (x.part < 2 && e < P) y[i] = fmaf(-row[e + P], s[e], y[i] * c[e]);
+            else if (x.part < 2 && e < 2 * P) y[i] = fmaf(row[e - P], s[e - P], y[i] * c[e - P]);
+          }
+        } else if (x.part < 2 && pairs > 0) {
+          const float4 c4 = cs[g0 + r][l], s4 = sn[g0 + r][l];
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+          if (apart) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) turn(y[i], y[i + 4], c[i], s[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < pairs) turn(y[2 * i], y[2 * i + 1], c[i], s[i]);
+          }
         }
+        if (x.part < 3)
+          store8<OUT>(x.dst + (g0 + r) * x.dst_step + o0 * OS, x.dst + (g0 + r) * x.dst_step + o1 * OS, y);
+      };
+      if (nr == RB) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r) work(r);
+      } else {
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+          if (r < nr) work(r);
       }
-      if (x.part < 3)
-        store8<OUT>(x.dst + (g0 + r) * x.dst_step + o0 * OS, x.dst + (g0 + r) * x.dst_step + o1 * OS, y);
-    };
-    if (nr == RB) {
-#pragma unroll
-      for (int r = 0; r < RB; ++r) work(r);
-    } else {
-#pragma unroll
-      for (int r = 0; r < RB; ++r)
-        if (r < nr) work(r);
     }
   }
 }

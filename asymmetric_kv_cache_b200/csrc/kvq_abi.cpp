@@ -17,6 +17,7 @@
 #include "kvq.h"
 #include "kvq_attend_plan.h"
 #include "kvq_internal.h"
+#include "kvq_operators.h"
 #include "kvq_reorder_plan.h"
 #include "kvq_split.h"
 
@@ -24,6 +25,7 @@ struct kvq_cache {
   kvq_config cfg;
   kvq::Geom geom;
   kvq::WsLayout ws;
+  kvq::AttendWs attend_ws;
   unsigned char* buf;
   size_t buf_bytes;
   std::vector<int32_t> lens;   // host mirror of the device lengths
@@ -174,9 +176,9 @@ kvq_status kvq_cache_required_bytes(const kvq_config* cfg, size_t* cache_bytes,
   kvq::Geom g;
   kvq::make_geom(*cfg, &g);
   kvq::WsLayout w;
-  kvq::make_cache_ws_layout(g, &w);
+  kvq::make_ws_layout(g, &w);
   if (cache_bytes) *cache_bytes = (size_t)g.total_bytes;
-  if (workspace_bytes) *workspace_bytes = (size_t)w.total;
+  if (workspace_bytes) *workspace_bytes = (size_t)kvq::make_attend_ws(g, w).total;
   return ok();
 }
 
@@ -201,7 +203,8 @@ kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_buf, size_t bytes, 
   c->cfg = *cfg;
   c->cfg.layout_version = KVQ_LAYOUT_VERSION;
   c->geom = g;
-  kvq::make_cache_ws_layout(g, &c->ws);
+  kvq::make_ws_layout(g, &c->ws);
+  c->attend_ws = kvq::make_attend_ws(g, c->ws);
   c->buf = static_cast<unsigned char*>(dev_buf);
   c->buf_bytes = bytes;
   c->lens.assign(cfg->max_seqs, 0);
@@ -451,9 +454,9 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   if (!q || !out || !workspace) return fail(KVQ_ERR_NULL, "q, out or workspace is NULL");
   if (!aligned(q, 16) || !aligned(out, 16)) return fail(KVQ_ERR_ALIGN, "q and out must be 16-byte aligned");
   if (!aligned(workspace, 256)) return fail(KVQ_ERR_ALIGN, "workspace must be 256-byte aligned");
-  if ((int64_t)ws_bytes < cache->ws.total)
+  if ((int64_t)ws_bytes < cache->attend_ws.total)
     return fail(KVQ_ERR_BUFFER_TOO_SMALL, "workspace has %zu bytes, needs %lld", ws_bytes,
-                (long long)cache->ws.total);
+                (long long)cache->attend_ws.total);
   if (cache->attend_ctas[0] == 0) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -468,6 +471,7 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   a.q_dtype = q_dtype;
   a.out = out;
   a.ws = static_cast<unsigned char*>(workspace);
+  a.tickets = reinterpret_cast<int32_t*>(a.ws + cache->attend_ws.tickets_off);
   a.scale = scale;
   a.cap = sc.cap;
   a.score_window = sc.window;

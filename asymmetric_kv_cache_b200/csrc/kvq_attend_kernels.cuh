@@ -31,7 +31,7 @@
 #include <atomic>
 
 #include "kvq_device.cuh"
-#include "kvq_internal.h"
+#include "kvq_operators.h"
 
 namespace kvq {
 
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kAttThreads, 4)
   const int unit = local / parts;
   __syncthreads();
   if (tid == 0) {
-    int* ticket = reinterpret_cast<int*>(a.ws + w.att_tickets_off) + seqs.unit_off[sq] + unit;
+    int* ticket = a.tickets + seqs.unit_off[sq] + unit;
     __threadfence();
     last = atomic_add_acq_rel_gpu(ticket, 1) == parts - 1;
     if (last) *ticket = 0;

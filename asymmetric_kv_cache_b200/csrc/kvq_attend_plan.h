@@ -4,7 +4,7 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "kvq_internal.h"
+#include "kvq_operators.h"
 
 namespace kvq {
 

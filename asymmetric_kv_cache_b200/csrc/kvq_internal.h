@@ -49,7 +49,6 @@ struct Geom {
 // last CTA to finish merges them (it resets the ticket to 0).
 struct WsLayout {
   int64_t err_off, units_off, tickets_off, partials_off, total;
-  int64_t att_tickets_off;   // kvq_attend's tickets (caches' workspaces), zero between calls
   int32_t units;       // split records
   int32_t slot_floats; // floats per partial slot: heads x (o[d], m, l, 2 pad)
 };
@@ -169,10 +168,6 @@ inline void make_ws_layout(const Geom& g, WsLayout* w) {
   w->total = align_up(w->partials_off + 2LL * kMaxDecodeCtas * w->slot_floats * 4, 256);
 }
 
-// The workspace of a cache: kvq_attend's partials start where the decode's do
-// and may be longer.
-inline void make_cache_ws_layout(const Geom& g, WsLayout* w);
-
 // ---- append / quantize ----------------------------------------------------
 // Per-sequence arguments of one append launch.  The current lengths are
 // not among them: the kernel reads them from the device copy, so a captured
@@ -231,102 +226,5 @@ cudaError_t launch_decode_fp16(const Geom& g, const WsLayout& w, const DecodeArg
 // address of that array on the current device (looked up on first use).
 constexpr int64_t kNoAllocScratchBytes = 8LL << 20;
 cudaError_t noalloc_scratch(void** ptr);
-
-// ---- attention of several new tokens per sequence ---------------------------
-// Sequences per attend / rotary launch (their arguments ride in the kernel
-// parameters).
-constexpr int kAttendMaxSeqs = 512;
-// Rows (query token, query head) of one unit: the N = 8 columns of the
-// P.V tile.
-constexpr int kAttendRows = 8;
-// Rows (D + 4 floats each) that the partials of one launch's split units may
-// take in a cache's workspace: 148 tensor-core units of 256 rows.
-constexpr int kAttendPartialRows = 148 * 256;
-// Units that a launch cuts into pieces at most (their tickets), and pieces of
-// a unit up to which the last of them to end merges them all.
-constexpr int kAttendTickets = 4096;
-constexpr int kAttendMergeParts = 32;
-// A sequence with at least this many rows per kv head goes to the tensor-core
-// kernel, if the call's such sequences give the other one at least so many
-// steps (8 rows against 32 keys of 128 channels; it does about 780 a us).
-// Measured, register tiles / tensor cores, us: 8 x 4113 keys, 32 query and 8 kv
-// heads: 32 rows 57 / 64, 64 rows 97 / 66; one context of 32768: 55 / 60, 91 /
-// 60; 64 x 2048: 169 / 272, 324 / 273; but 16 x 1000 keys of 64 channels and 4
-// kv heads, 64 rows: 20 / 35 (16 thousand steps; the tensor-core kernel's
-// start and end take 25 us).
-constexpr int kAttendTcRows = 48;
-constexpr int kAttendTcSteps = 32768;
-
-inline void make_cache_ws_layout(const Geom& g, WsLayout* w) {
-  make_ws_layout(g, w);
-  const int64_t end = align_up(w->partials_off + 4LL * kAttendPartialRows * (g.d + 4), 256);
-  w->att_tickets_off = end > w->total ? end : w->total;
-  w->total = align_up(w->att_tickets_off + 4LL * kAttendTickets, 256);
-}
-
-struct AttendArgs {
-  const unsigned char* cache;
-  const void* q;             // [rows][hq][d]
-  int32_t q_dtype;
-  void* out;                 // fp16 [rows][hq][d]
-  unsigned char* ws;
-  float scale, cap;          // cap = 0: none
-  int32_t score_window;      // 0: none
-  const float* slopes;       // [hq] or NULL
-  const int32_t* prefix;     // [n_seq] or NULL
-  int32_t residual;          // queries that fp16 does not hold exactly
-};
-
-// Sequence i of a launch is the cache's seq0 + i; its query rows start at
-// row_off[i] (n_q[i] of them) and its pieces at piece_off[i]: per (kv head,
-// row tile) the same number of pieces, tile after tile.
-struct AttendSeqs {
-  int32_t n, seq0;
-  int32_t unit_rows;         // kAttendRows, or 256 / 128 (tensor cores)
-  int32_t slot_rows;         // rows of a piece's partial slot
-  int32_t merge_here;        // the last piece of a unit merges them (no merge kernel)
-  int32_t row_off[kAttendMaxSeqs];
-  int32_t n_q[kAttendMaxSeqs];
-  int32_t piece_off[kAttendMaxSeqs + 1];
-  int32_t unit_off[kAttendMaxSeqs + 1];   // units before the sequence's
-};
-
-cudaError_t attend_max_ctas(const Geom& g, int* max_ctas);
-cudaError_t launch_attend(const Geom& g, const WsLayout& w, const AttendArgs& a,
-                          const AttendSeqs& s, bool split, cudaStream_t stream);
-#define KVQ_ATTEND_DECLARE(D_, KB_, VB_, G_)                                          \
-  cudaError_t attend_max_ctas_##D_##_##KB_##_##VB_##_##G_(int* out);                  \
-  cudaError_t launch_attend_##D_##_##KB_##_##VB_##_##G_(                              \
-      const Geom& g, const WsLayout& w, const AttendArgs& a, const AttendSeqs& s,     \
-      cudaStream_t stream);
-KVQ_DECODE_FOR_EACH(KVQ_ATTEND_DECLARE)
-
-// ---- norms of query and key heads with the position rotation ----------------
-struct RotaryArgs {
-  const void *q, *k, *v;     // v may be NULL
-  int64_t q_stride, k_stride, v_stride;   // elements between rows
-  void *q_out, *k_out, *v_out;
-  const void *q_weight, *k_weight;        // [d] of the input type, or NULL
-  float eps;
-  const float* inv_freq;     // [n_pairs]
-  int32_t n_pairs, interleaved;
-  const int32_t* positions;  // [n_axes][rows], or NULL: from the lengths
-  int32_t n_axes, sections[4];
-  const int32_t* lens;
-  int64_t rows;              // of the whole call
-  int32_t hq, hkv;
-};
-struct RotarySeqs {
-  int32_t n, seq0;
-  int64_t row0;              // the launch's first row
-  int32_t row_off[kAttendMaxSeqs];        // from row0
-};
-cudaError_t launch_norm_rotary(int d, int dtype, int out_dtype, const RotaryArgs& a,
-                               const RotarySeqs& seqs, int rows, cudaStream_t stream);
-
-// ---- reordering of sequences ---------------------------------------------
-struct ReorderMoves;         // kvq_reorder_plan.h
-cudaError_t launch_reorder(const Geom& g, unsigned char* cache, const ReorderMoves& mv,
-                           int shared_tokens, int64_t bytes, cudaStream_t stream);
 
 }  // namespace kvq

@@ -19,7 +19,7 @@
 #include <algorithm>
 
 #include "kvq_device.cuh"
-#include "kvq_internal.h"
+#include "kvq_operators.h"
 #include "kvq_reorder_plan.h"
 
 namespace kvq {

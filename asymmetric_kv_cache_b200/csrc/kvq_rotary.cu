@@ -22,7 +22,7 @@
 #include <cuda_fp16.h>
 
 #include "kvq_device.cuh"
-#include "kvq_internal.h"
+#include "kvq_operators.h"
 
 namespace kvq {
 namespace {

@@ -213,8 +213,9 @@ KVQ_API const char* kvq_last_error(void);
  * Errors: KVQ_ERR_NULL, KVQ_ERR_CONFIG. */
 KVQ_API kvq_status kvq_layout_for(const kvq_config* cfg, kvq_layout* out);
 
-/* Bytes the caller must provide: the cache buffer and the decode workspace
- * (split partials, per-unit split records and an error word).  Either output
+/* Bytes the caller must provide: the cache buffer and the workspace of
+ * kvq_decode and kvq_attend (split partials, per-unit split records, tickets
+ * and an error word).  Either output
  * pointer may be NULL.  Host only.  Errors: KVQ_ERR_NULL, KVQ_ERR_CONFIG. */
 KVQ_API kvq_status kvq_cache_required_bytes(const kvq_config* cfg, size_t* cache_bytes,
                                     size_t* workspace_bytes);

@@ -15,7 +15,7 @@ STUB = r"""
 #include <cstring>
 #include <vector>
 #include <cuda_runtime.h>
-#include "kvq_internal.h"
+#include "kvq_operators.h"
 #include "kvq_reorder_plan.h"
 
 static std::vector<int32_t> g_log;          // what the launches were given

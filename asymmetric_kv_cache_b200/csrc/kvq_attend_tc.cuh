@@ -384,7 +384,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int t0 = (int)((int64_t)all_tiles * part / parts), t1 = (int)((int64_t)all_tiles * (part + 1) / parts);
   const int nt = t1 - t0;
 
-  if (tid == 0) {
+  // the copy warp's first tiles are on their way before anything else
+  auto copy_tile = [&](int t) {            // one lane
+    const unsigned char* blocks =
+        a.cache + g.blocks_off + ((int64_t)seq * g.hkv + h) * g.max_groups * g.block_bytes;
+    const int slot = t % C::NRAW;
+    uint32_t bytes[2] = {0u, 0u};
+    int grp[2];
+#pragma unroll
+    for (int i = 0; i < 64 / G; ++i) {
+      const int c = 2 * (t0 + t) + i;
+      if (c >= keys.nblk * keys.per) continue;
+      grp[i] = keys.group(c);
+      bytes[i] = KB == 4 && g.akvq_delta && akvq_key_bits(grp[i], n, G, g.akvq_delta) == 2 ? g.a2_bytes
+                                                                                          : g.block_bytes;
+    }
+    uint64_t* bar = &bars[C::B_RF + slot];
+    if (bytes[0] + bytes[1] > 0) mbar_arrive_expect_tx(bar, bytes[0] + bytes[1]);
+    else mbar_arrive(bar);
+#pragma unroll
+    for (int i = 0; i < 64 / G; ++i)
+      if (bytes[i] > 0)
+        bulk_copy_g2s(smem + C::RAW_OFF + slot * C::RAW + i * (C::RAW / 2),
+                      blocks + (int64_t)grp[i] * g.block_bytes, bytes[i], bar);
+  };
+  if (warp == 18 && lane == 0) {
     for (int s = 0; s < C::NST; ++s) mbar_init(&bars[C::B_EMPTY + s], nx);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[C::B_S + x], 1);
@@ -395,6 +419,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&bars[C::B_RE + s], 4);
     }
     fence_mbar_init();
+    for (int t = 0; t < min(nt, C::NRAW); ++t) copy_tile(t);
   }
   if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -409,32 +434,66 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   unsigned char* io = smem + (warp & 7) * 32 * C::IO_ROW;
   if (warp < 8 && X < nx) {
     constexpr int V = D / 32;
-    // eight rows' loads at a time
+    // eight rows' loads at a time, as they are in memory: converting each where
+    // it is loaded took a latency a row, 20000 cycles in all.  Rows past the
+    // last repeat it (their results go nowhere).
+    const int es = a.q_dtype == KVQ_FP32 ? 4 : 2;
+    int qi = (r0 + min(wrow, nr - 1)) / g.gqa, hh = (r0 + min(wrow, nr - 1)) % g.gqa;
+    const unsigned char* qp = reinterpret_cast<const unsigned char*>(a.q) +
+                              (((int64_t)(seqs.row_off[sq] + qi) * g.hq + h * g.gqa + hh) * D + lane * V) * es;
+    const int64_t next_token = ((int64_t)g.hq - g.gqa + 1) * D * es;
     for (int i0 = 0; i0 < 32; i0 += 8) {
-      float y[8][V];
+      uint32_t raw[8][V];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = r0 + wrow + i0 + i;
-#pragma unroll
-        for (int k = 0; k < V; ++k) y[i][k] = 0.f;
-        if (wrow + i0 + i < nr)
-          att_load_q<V>(a.q, ((int64_t)(seqs.row_off[sq] + r / g.gqa) * g.hq + h * g.gqa + r % g.gqa) * D + lane * V,
-                        a.q_dtype, y[i]);
+        if (es == 4) {
+          if constexpr (V == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(qp);
+            raw[i][0] = x.x; raw[i][1] = x.y; raw[i][2] = x.z; raw[i][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(qp);
+            raw[i][0] = x.x; raw[i][1] = x.y;
+          }
+        } else if constexpr (V == 4) {
+          const uint2 x = *reinterpret_cast<const uint2*>(qp);
+          raw[i][0] = x.x; raw[i][1] = x.y;
+        } else {
+          raw[i][0] = *reinterpret_cast<const uint32_t*>(qp);
+        }
+        if (wrow + i0 + i + 1 < nr) {
+          const bool wrap = ++hh == g.gqa;
+          hh = wrap ? 0 : hh;
+          qp += wrap ? next_token : (int64_t)D * es;
+        }
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (g.rotate) {
-          fwht_lanes<D, V>(y[i], lane);
+        float y[V];
+        if (es == 4) {
 #pragma unroll
-          for (int k = 0; k < V; ++k) y[i][k] *= rot_scale<D>();
+          for (int k = 0; k < V; ++k) y[k] = __uint_as_float(raw[i][k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V / 2; ++k) {
+            const float2 f = a.q_dtype == KVQ_FP16
+                                 ? __half22float2(u32_as_h2(raw[i][k]))
+                                 : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k]));
+            y[2 * k] = f.x;
+            y[2 * k + 1] = f.y;
+          }
+        }
+        if (g.rotate) {
+          fwht_lanes<D, V>(y, lane);
+#pragma unroll
+          for (int k = 0; k < V; ++k) y[k] *= rot_scale<D>();
         }
 #pragma unroll
         for (int k = 0; k < V; k += 2) {
-          const uint32_t hi = pack_h2(y[i][k], y[i][k + 1]);
+          const uint32_t hi = pack_h2(y[k], y[k + 1]);
           const float2 f = __half22float2(u32_as_h2(hi));
           uint32_t* dst = reinterpret_cast<uint32_t*>(io + (i0 + i) * C::IO_ROW) + (lane * V + k) / 2;
           dst[0] = hi;
-          dst[D / 2] = pack_h2(y[i][k] - f.x, y[i][k + 1] - f.y);
+          if (exact) dst[D / 2] = pack_h2(y[k] - f.x, y[k + 1] - f.y);
         }
       }
     }
@@ -586,7 +645,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // done (the last key tile's stage is free: nobody waits for later phases)
       if (nt > 0) att_tc_wait(&bars[C::B_EMPTY + (nt - 1) % C::NST], (nt - 1) / C::NST & 1, ok, err, lane);
       att_tc_fence_after();
+      constexpr int V = D / 32;
       float* row = reinterpret_cast<float*>(io + lane * C::IO_ROW);
+      // a whole unit of a cache that is not rotated: the thread divides its
+      // row, fp16 goes through shared memory, and rows go out eight at a time
+      // (a row after the other through attend_store_row took 15000 cycles)
+      const bool whole = parts == 1 && !g.rotate;
+      const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -597,29 +662,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<uint4*>(row + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 16; ++i) {
+            const float x = __uint_as_float(o[2 * i]), y = __uint_as_float(o[2 * i + 1]);
+            o[i] = inv != 0.f ? pack_h2(x * inv, y * inv) : 0u;
+          }
+        }
+        uint4* dst = reinterpret_cast<uint4*>(row) + (whole ? 4 : 8) * c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < 4 || !whole) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
       __syncwarp();
-      constexpr int V = D / 32;
-      for (int i = 0; i < 32 && wrow + i < nr; ++i) {
-        const float li = __shfl_sync(0xffffffffu, l, i), mi = __shfl_sync(0xffffffffu, m, i);
-        const float* src = reinterpret_cast<const float*>(io + i * C::IO_ROW) + lane * V;
-        float y[V];
+      if (whole) {
+        const int rows = min(32, nr - wrow);
+        int hh = (r0 + min(wrow, nr - 1)) % g.gqa;
+        unsigned char* op = reinterpret_cast<unsigned char*>(a.out) +
+                            (((int64_t)(seqs.row_off[sq] + (r0 + min(wrow, nr - 1)) / g.gqa) * g.hq + h * g.gqa + hh) * D +
+                             lane * V) * 2;
+        const int64_t next_token = ((int64_t)g.hq - g.gqa + 1) * D * 2;
+        for (int i0 = 0; i0 < rows; i0 += 8) {
+          uint32_t x[8][V / 2];
 #pragma unroll
-        for (int k = 0; k < V; ++k) y[k] = src[k];
-        if (parts > 1) {
-          float* ps = reinterpret_cast<float*>(a.ws + w.partials_off) +
-                      ((int64_t)blockIdx.x * seqs.slot_rows + wrow + i) * (D + 4);
+          for (int i = 0; i < 8; ++i) lds_words<V / 2>(reinterpret_cast<const uint32_t*>(io + (i0 + i) * C::IO_ROW) + lane * (V / 2), x[i]);
 #pragma unroll
-          for (int k = 0; k < V; ++k) ps[lane * V + k] = y[k];
-          if (lane == 0) {
-            ps[D] = mi;
-            ps[D + 1] = li;
+          for (int i = 0; i < 8; ++i) {
+            if (i0 + i < rows) {
+              if constexpr (V == 4) *reinterpret_cast<uint2*>(op) = make_uint2(x[i][0], x[i][1]);
+              else *reinterpret_cast<uint32_t*>(op) = x[i][0];
+            }
+            const bool wrap = ++hh == g.gqa;
+            hh = wrap ? 0 : hh;
+            op += wrap ? next_token : (int64_t)D * 2;
           }
-        } else {
-          attend_store_row<D>(g, a, seqs, sq, h, r0 + wrow + i, y, li, lane);
+        }
+      } else {
+        for (int i = 0; i < 32 && wrow + i < nr; ++i) {
+          const float li = __shfl_sync(0xffffffffu, l, i), mi = __shfl_sync(0xffffffffu, m, i);
+          const float* src = reinterpret_cast<const float*>(io + i * C::IO_ROW) + lane * V;
+          float y[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) y[k] = src[k];
+          if (parts > 1) {
+            float* ps = reinterpret_cast<float*>(a.ws + w.partials_off) +
+                        ((int64_t)blockIdx.x * seqs.slot_rows + wrow + i) * (D + 4);
+#pragma unroll
+            for (int k = 0; k < V; ++k) ps[lane * V + k] = y[k];
+            if (lane == 0) {
+              ps[D] = mi;
+              ps[D + 1] = li;
+            }
+          } else {
+            attend_store_row<D>(g, a, seqs, sq, h, r0 + wrow + i, y, li, lane);
+          }
         }
       }
     }
@@ -715,31 +811,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     } else if (warp == 18) {
     // ====== bulk copies of the tiles' blocks ======
-    const unsigned char* blocks =
-        a.cache + g.blocks_off + ((int64_t)seq * g.hkv + h) * g.max_groups * g.block_bytes;
-    for (int t = 0; t < nt; ++t) {
-      const int slot = t % C::NRAW;
-      if (t >= C::NRAW) att_tc_wait(&bars[C::B_RE + slot], (t / C::NRAW - 1) & 1, ok, err, lane);
-      if (lane == 0) {
-        uint32_t bytes[2] = {0u, 0u};
-        int grp[2];
-#pragma unroll
-        for (int i = 0; i < 64 / G; ++i) {
-          const int c = 2 * (t0 + t) + i;
-          if (c >= keys.nblk * keys.per) continue;
-          grp[i] = keys.group(c);
-          bytes[i] = KB == 4 && g.akvq_delta && akvq_key_bits(grp[i], n, G, g.akvq_delta) == 2 ? g.a2_bytes
-                                                                                            : g.block_bytes;
-        }
-        uint64_t* bar = &bars[C::B_RF + slot];
-        if (bytes[0] + bytes[1] > 0) mbar_arrive_expect_tx(bar, bytes[0] + bytes[1]);
-        else mbar_arrive(bar);
-#pragma unroll
-        for (int i = 0; i < 64 / G; ++i)
-          if (bytes[i] > 0)
-            bulk_copy_g2s(smem + C::RAW_OFF + slot * C::RAW + i * (C::RAW / 2),
-                          blocks + (int64_t)grp[i] * g.block_bytes, bytes[i], bar);
-      }
+    for (int t = C::NRAW; t < nt; ++t) {
+      att_tc_wait(&bars[C::B_RE + t % C::NRAW], (t / C::NRAW - 1) & 1, ok, err, lane);
+      if (lane == 0) copy_tile(t);
       __syncwarp();
     }
     // copies in flight land before the shared memory goes away (after a

@@ -434,68 +434,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   unsigned char* io = smem + (warp & 7) * 32 * C::IO_ROW;
   if (warp < 8 && X < nx) {
     constexpr int V = D / 32;
-    // eight rows' loads at a time, as they are in memory: converting each where
-    // it is loaded took a latency a row, 20000 cycles in all.  Rows past the
-    // last repeat it (their results go nowhere).
-    const int es = a.q_dtype == KVQ_FP32 ? 4 : 2;
-    int qi = (r0 + min(wrow, nr - 1)) / g.gqa, hh = (r0 + min(wrow, nr - 1)) % g.gqa;
-    const unsigned char* qp = reinterpret_cast<const unsigned char*>(a.q) +
-                              (((int64_t)(seqs.row_off[sq] + qi) * g.hq + h * g.gqa + hh) * D + lane * V) * es;
-    const int64_t next_token = ((int64_t)g.hq - g.gqa + 1) * D * es;
-    for (int i0 = 0; i0 < 32; i0 += 8) {
-      uint32_t raw[8][V];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (es == 4) {
-          if constexpr (V == 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(qp);
-            raw[i][0] = x.x; raw[i][1] = x.y; raw[i][2] = x.z; raw[i][3] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(qp);
-            raw[i][0] = x.x; raw[i][1] = x.y;
-          }
-        } else if constexpr (V == 4) {
-          const uint2 x = *reinterpret_cast<const uint2*>(qp);
-          raw[i][0] = x.x; raw[i][1] = x.y;
-        } else {
-          raw[i][0] = *reinterpret_cast<const uint32_t*>(qp);
-        }
-        if (wrow + i0 + i + 1 < nr) {
-          const bool wrap = ++hh == g.gqa;
-          hh = wrap ? 0 : hh;
-          qp += wrap ? next_token : (int64_t)D * es;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+    // Short code: it runs once per unit, and its instructions come from far away
+    // (rows converted in registers, eight at a time, took 13600 cycles).  Rows
+    // past the last repeat it (their results go nowhere).
+    const int es = a.q_dtype == KVQ_FP32 ? 4 : 2, cpr = D * es / 16;
+#pragma unroll 1
+    for (int i = lane / cpr; i < 32; i += 32 / cpr) {
+      const int r = r0 + min(wrow + i, nr - 1);
+      const int64_t at = ((int64_t)(seqs.row_off[sq] + r / g.gqa) * g.hq + h * g.gqa + r % g.gqa) * D * es;
+      cp_async16(io + i * C::IO_ROW + lane % cpr * 16,
+                 reinterpret_cast<const unsigned char*>(a.q) + at + lane % cpr * 16, 16);
+    }
+    cp_async_wait_all();
+    __syncwarp();
+    if (g.rotate) {                         // to fp32, in place
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i) {
         float y[V];
-        if (es == 4) {
+        att_load_q<V>(io + i * C::IO_ROW, lane * V, a.q_dtype, y);
+        fwht_lanes<D, V>(y, lane);
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < V; ++k) y[k] = __uint_as_float(raw[i][k]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < V / 2; ++k) {
-            const float2 f = a.q_dtype == KVQ_FP16
-                                 ? __half22float2(u32_as_h2(raw[i][k]))
-                                 : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k]));
-            y[2 * k] = f.x;
-            y[2 * k + 1] = f.y;
-          }
-        }
-        if (g.rotate) {
-          fwht_lanes<D, V>(y, lane);
-#pragma unroll
-          for (int k = 0; k < V; ++k) y[k] *= rot_scale<D>();
-        }
-#pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          const uint32_t hi = pack_h2(y[k], y[k + 1]);
-          const float2 f = __half22float2(u32_as_h2(hi));
-          uint32_t* dst = reinterpret_cast<uint32_t*>(io + (i0 + i) * C::IO_ROW) + (lane * V + k) / 2;
-          dst[0] = hi;
-          if (exact) dst[D / 2] = pack_h2(y[k] - f.x, y[k + 1] - f.y);
-        }
+        for (int k = 0; k < V; ++k)
+          reinterpret_cast<float*>(io + i * C::IO_ROW)[lane * V + k] = y[k] * rot_scale<D>();
       }
+      __syncwarp();
     }
   }
   att_tc_fence_before();
@@ -505,17 +468,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
   if (warp < 8 && X < nx) {
     const uint4* src = reinterpret_cast<const uint4*>(io + lane * C::IO_ROW);
-    for (int x = 0; x < (exact ? 2 : 1); ++x) {
+    const uint32_t tq = tm + lanes + C::T_Q + X * (D / 2);
+#pragma unroll 1
+    for (int c = 0; c < D / 64; ++c) {      // 64 channels
+      uint32_t r[32];
+      if (exact) {                          // value and residual
+        uint32_t lo[32];
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t r[32];
+        for (int i = 0; i < 16; ++i) {
+          const uint4 v = src[16 * c + i];
+          const float f[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            r[2 * i + k] = pack_h2(f[2 * k], f[2 * k + 1]);
+            const float2 b = __half22float2(u32_as_h2(r[2 * i + k]));
+            lo[2 * i + k] = pack_h2(f[2 * k] - b.x, f[2 * k + 1] - b.y);
+          }
+        }
+        att_tc_st32(tq + D / 2 + 32 * c, lo);
+      } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint4 v = src[x * (D / 8) + 8 * c + i];
+          const uint4 v = src[8 * c + i];
           r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
         }
-        att_tc_st32(tm + lanes + C::T_Q + (X + x) * (D / 2) + 32 * c, r);
+        if (a.q_dtype == KVQ_BF16) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]));
+            r[i] = pack_h2(f.x, f.y);
+          }
+        }
       }
+      att_tc_st32(tq + 32 * c, r);
     }
     att_tc_wait_st();
   }
@@ -676,7 +661,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       __syncwarp();
       if (whole) {
-        const int rows = min(32, nr - wrow);
+        const int rows = min(32, nr - wrow);         // (none of a warp behind the last row)
         int hh = (r0 + min(wrow, nr - 1)) % g.gqa;
         unsigned char* op = reinterpret_cast<unsigned char*>(a.out) +
                             (((int64_t)(seqs.row_off[sq] + (r0 + min(wrow, nr - 1)) / g.gqa) * g.hq + h * g.gqa + hh) * D +
@@ -698,23 +683,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       } else {
-        for (int i = 0; i < 32 && wrow + i < nr; ++i) {
-          const float li = __shfl_sync(0xffffffffu, l, i), mi = __shfl_sync(0xffffffffu, m, i);
+        const int rows = min(32, nr - wrow);
+        float* ps = reinterpret_cast<float*>(a.ws + w.partials_off) +
+                    ((int64_t)blockIdx.x * seqs.slot_rows + wrow) * (D + 4);
+        if (parts > 1 && lane < rows) {
+          ps[lane * (D + 4) + D] = m;
+          ps[lane * (D + 4) + D + 1] = l;
+        }
+#pragma unroll 4
+        for (int i = 0; i < rows; ++i) {
           const float* src = reinterpret_cast<const float*>(io + i * C::IO_ROW) + lane * V;
           float y[V];
 #pragma unroll
           for (int k = 0; k < V; ++k) y[k] = src[k];
           if (parts > 1) {
-            float* ps = reinterpret_cast<float*>(a.ws + w.partials_off) +
-                        ((int64_t)blockIdx.x * seqs.slot_rows + wrow + i) * (D + 4);
 #pragma unroll
-            for (int k = 0; k < V; ++k) ps[lane * V + k] = y[k];
-            if (lane == 0) {
-              ps[D] = mi;
-              ps[D + 1] = li;
-            }
+            for (int k = 0; k < V; ++k) ps[i * (D + 4) + lane * V + k] = y[k];
           } else {
-            attend_store_row<D>(g, a, seqs, sq, h, r0 + wrow + i, y, li, lane);
+            attend_store_row<D>(g, a, seqs, sq, h, r0 + wrow + i, y, __shfl_sync(0xffffffffu, l, i), lane);
           }
         }
       }

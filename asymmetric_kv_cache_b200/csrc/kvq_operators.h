@@ -20,16 +20,16 @@ constexpr int kAttendPartialRows = 148 * 256;
 // a unit up to which the last of them to end merges them all.
 constexpr int kAttendTickets = 4096;
 constexpr int kAttendMergeParts = 32;
-// A sequence with at least this many rows per kv head goes to the tensor-core
-// kernel, if the call's such sequences give the other one at least so many
-// steps (8 rows against 32 keys of 128 channels; it does about 780 a us).
-// Measured, register tiles / tensor cores, us: 8 x 4113 keys, 32 query and 8 kv
-// heads: 32 rows 57 / 64, 64 rows 97 / 66; one context of 32768: 55 / 60, 91 /
-// 60; 64 x 2048: 169 / 272, 324 / 273; but 16 x 1000 keys of 64 channels and 4
-// kv heads, 64 rows: 20 / 35 (16 thousand steps; the tensor-core kernel's
-// start and end take 25 us).
-constexpr int kAttendTcRows = 48;
-constexpr int kAttendTcSteps = 32768;
+// A sequence with at least this many rows per kv head (more than four tiles of
+// kAttendRows) goes to the tensor-core kernel, if the call's such sequences
+// give the other one at least so many steps (8 rows against 32 keys of 128
+// channels; it does about 780 a us).  Measured, register tiles / tensor cores,
+// us, 32 query and 8 kv heads of 128: 8 x 4113 keys: 24 rows 41 / 50, 32 rows
+// 55 / 52, 48 rows 93 / 53; one context of 32768: 43 / 51, 53 / 51, 71 / 50;
+// 64 x 2048: 132 / 192, 166 / 193, 244 / 193; 16 x 1000: 29 / 28, 29 / 28, 43 /
+// 28; with 4 kv heads of 64 (6 thousand steps at 48 rows) 18 / 26.
+constexpr int kAttendTcRows = 33;
+constexpr int kAttendTcSteps = 16384;
 
 // The workspace of a cache: kvq_attend's partials start where the decode's do
 // and may be longer; its tickets (zero between calls) follow.  total: all of

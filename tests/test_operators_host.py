@@ -70,7 +70,7 @@ def test_attend_plan(host, seed, dt):
     first = [sum(n_q[:b]) for b in range(seqs)]
     log, seen = host.log(), {}
     keys = lambda b: min(lens[b], window + n_q[b]) if window else lens[b]  # noqa: E731
-    steps = sum(hkv * -(-n_q[b] * gqa // 8) * (keys(b) // 32 + 1) for b in range(seqs) if n_q[b] * gqa >= 48)
+    steps = sum(hkv * -(-n_q[b] * gqa // 8) * (keys(b) // 32 + 1) for b in range(seqs) if n_q[b] * gqa >= 33)
     while log:
         kind, n, seq0, split, pieces, unit, slot, residual = log[:8]
         assert kind == 1 and residual == (dt == 2) and unit in ((8, 128) if residual else (8, 256))
@@ -83,7 +83,7 @@ def test_attend_plan(host, seed, dt):
             rows, got = n_q[b] * gqa, offs[i + 1] - offs[i]
             if got == 0:
                 continue
-            assert b not in seen and (unit > 8) == (rows >= 48 and steps >= 32768)
+            assert b not in seen and (unit > 8) == (rows >= 33 and steps >= 16384)
             seen[b] = True
             units = hkv * -(-rows // unit)
             assert got % units == 0 and got >= units

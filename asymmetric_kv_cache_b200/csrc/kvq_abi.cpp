@@ -418,6 +418,14 @@ kvq_status kvq_decode_noalloc(kvq_cache* cache, const void* q, kvq_dtype q_dtype
   return ok();
 }
 
+namespace {
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+}  // namespace
+
 kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const int32_t* n_q,
                       int32_t n_seq, const kvq_scores* scores, void* out, void* workspace,
                       size_t ws_bytes, void* stream) {
@@ -454,6 +462,8 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   if (!q || !out || !workspace) return fail(KVQ_ERR_NULL, "q, out or workspace is NULL");
   if (!aligned(q, 16) || !aligned(out, 16)) return fail(KVQ_ERR_ALIGN, "q and out must be 16-byte aligned");
   if (!aligned(workspace, 256)) return fail(KVQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  if (overlap(q, total * g.hq * g.d * (q_dtype == KVQ_FP32 ? 4 : 2), out, total * g.hq * g.d * 2))
+    return fail(KVQ_ERR_ARG, "out overlaps q");
   if ((int64_t)ws_bytes < cache->attend_ws.total)
     return fail(KVQ_ERR_BUFFER_TOO_SMALL, "workspace has %zu bytes, needs %lld", ws_bytes,
                 (long long)cache->attend_ws.total);
@@ -498,14 +508,6 @@ kvq_status kvq_attend(kvq_cache* cache, const void* q, kvq_dtype q_dtype, const 
   }
   return ok();
 }
-
-namespace {
-// Whether [a, a + na) and [b, b + nb) share a byte.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-}  // namespace
 
 kvq_status kvq_norm_rotary(kvq_cache* cache, const void* q, int64_t q_stride, const void* k,
                            int64_t k_stride, const void* v, int64_t v_stride, kvq_dtype dtype,

@@ -50,6 +50,14 @@ class KvqLayout(ctypes.Structure):
         "akvq_vcodes_offset", "akvq_vscale_offset", "akvq_vmin_offset")]
 
 
+def _int32s(values, name: str):
+    """A C array of integers that fit (ctypes would cut off the upper bits of others)."""
+    arr = (ctypes.c_int32 * len(values))(*values)
+    if arr[:] != list(values):
+        raise ValueError(f"{name} must be 32-bit integers")
+    return arr
+
+
 class KvqScores(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("window", ctypes.c_int32),
                 ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
@@ -311,10 +319,10 @@ class KVQCache:
         if dt is None:
             raise ValueError("q must be fp16, bf16 or fp32")
         sp, n_seq = self.spec, len(n_q)
-        arr = (ctypes.c_int32 * n_seq)(*n_q)
+        arr = _int32s(n_q, "n_q")
         shape = (sum(n_q), sp.n_q_heads, sp.head_dim)
         qp = self._ptr(q, "q", None, shape)
-        sc = KvqScores(scale, cap, window,
+        sc = KvqScores(scale, cap, _int32s((window,), "window")[0],
                        None if slopes is None else self._ptr(slopes, "slopes", torch.float32, (sp.n_q_heads,)),
                        None if prefix is None else self._ptr(prefix, "prefix", torch.int32, (n_seq,)))
         if out is None:
@@ -353,7 +361,7 @@ class KVQCache:
         if dt is None or odt is None:
             raise ValueError("rows and outputs must be fp16, bf16 or fp32")
         sp, n, n_seq, d, kind = self.spec, sum(n_new), len(n_new), self.spec.head_dim, q.dtype
-        arr = (ctypes.c_int32 * n_seq)(*n_new)
+        arr = _int32s(n_new, "n_new")
         q_shape, k_shape = (n, sp.n_q_heads, d), (n, sp.n_kv_heads, d)
         qp, qs = self._rows(q, "q", kind, q_shape)
         kp, ks = self._rows(k, "k", kind, k_shape)
@@ -374,7 +382,7 @@ class KVQCache:
                 raise ValueError(f"sections must give the pairs of {axes} axes")
             rot.positions = self._ptr(positions, "positions", torch.int32)
             rot.n_axes = axes
-            rot.sections[:axes] = sections
+            rot.sections[:axes] = _int32s(sections, "sections")[:]
         elif sections is not None:
             raise ValueError("sections go with positions")
         if out is None:
@@ -393,8 +401,8 @@ class KVQCache:
     def reorder(self, parent, shared: int = 0, stream=None):
         """Sequence b takes over sequence ``parent[b]``, all at once (kvq_reorder); the first
         ``shared`` tokens of moving sequences and their parents are the same already."""
-        n_seq = len(parent)
-        self._launch("kvq_reorder", kvq_reorder, stream, self._h, (ctypes.c_int32 * n_seq)(*parent), n_seq, int(shared))
+        self._launch("kvq_reorder", kvq_reorder, stream, self._h, _int32s(parent, "parent"), len(parent),
+                     _int32s((shared,), "shared")[0])
 
     def workspace_status(self, stream=None) -> int:
         return kvq_workspace_status(self.workspace.data_ptr(), _stream(stream))

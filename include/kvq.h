@@ -350,7 +350,9 @@ typedef struct {
  * conversation.  A row that sees no key gets 0.
  * q: device [sum_b n_q[b], n_q_heads, d], sequences concatenated in order b
  * (fp16, bf16 or fp32, 16-byte aligned), read only; out: device, the same
- * shape, fp16, written.  n_q: host array of n_seq counts, each at most the
+ * shape, fp16, written, not overlapping q.  The kernels hold a query in fp16
+ * (fp32 and rotated ones as a value and its residual): magnitudes above 65504
+ * become infinite, bf16 ones below 2^-14 are held to 2^-25.  n_q: host array of n_seq counts, each at most the
  * sequence's length (0 skips the sequence), read before the call returns;
  * scores: host struct or NULL, read before the call returns.
  * workspace, ws_bytes: as for kvq_decode (the same buffer serves both; calls

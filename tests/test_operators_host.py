@@ -21,7 +21,10 @@ def host(tmp_path_factory):
 
 
 # ---------------------------------------------------------------- attend
-def _attend(host, h, n_q, q=ot.Host.PTR, dt=0, out=ot.Host.PTR, ws=ot.Host.PTR, ws_bytes=None, n_seq=None, **sc):
+OUT = ot.Host.PTR + (1 << 40)
+
+
+def _attend(host, h, n_q, q=ot.Host.PTR, dt=0, out=OUT, ws=ot.Host.PTR, ws_bytes=None, n_seq=None, **sc):
     scores = host.kvq.KvqScores(**sc)
     return host.lib.kvq_attend(h, ctypes.c_void_p(q), dt, host.ints(n_q) if n_q is not None else None,
                                len(n_q or []) if n_seq is None else n_seq, ctypes.byref(scores), ctypes.c_void_p(out),
@@ -41,6 +44,7 @@ def test_attend_refusals(host):
         (dict(n_q=[1], ws_bytes=host.ws - 1), H.SMALL), (dict(n_q=[1], scale=-1.0), H.ARG),
         (dict(n_q=[1], scale=float("nan")), H.ARG), (dict(n_q=[1], cap=-2.0), H.ARG),
         (dict(n_q=[1], cap=float("inf")), H.ARG), (dict(n_q=[1], window=-1), H.ARG),
+        (dict(n_q=[1], out=H.PTR), H.ARG), (dict(n_q=[2], out=H.PTR + 256), H.ARG),
         (dict(n_q=[1], scale=3e38), H.ARG), (dict(n_q=[1], cap=2e38), H.ARG), (dict(n_q=[1], scale=1.0, cap=1e-39), H.ARG),
     ]
     for kw, want in cases:
@@ -50,6 +54,22 @@ def test_attend_refusals(host):
     assert not host.log()                       # nothing was launched
     assert _attend(host, h, n_q=[0, 0, 0], q=0, out=0, ws=0) == 0 and not host.log()
     assert _attend(host, h, n_q=[100, 1, 0, 300]) == 0 and host.log()
+
+
+def test_out_beside_q(host):
+    """out may start where q ends (n_q rows of 32 heads of 128) and end where q starts, and share no byte."""
+    h, P, row = host.cache([100]), ot.Host.PTR, 32 * 128 * 2
+    assert _attend(host, h, n_q=[3], out=P + 3 * row) == 0 and _attend(host, h, n_q=[3], q=P + 3 * row, out=P) == 0
+    assert _attend(host, h, n_q=[3], dt=2, out=P + 3 * row) == ot.Host.ARG
+    assert _attend(host, h, n_q=[3], dt=2, out=P + 6 * row) == 0
+    assert _attend(host, h, n_q=[3], out=P + 3 * row - 16) == ot.Host.ARG
+
+
+@pytest.mark.parametrize("values", [[2 ** 32], [1, 2 ** 31], [-2 ** 31 - 1], [0, 2 ** 32 + 1]])
+def test_integers_keep_their_upper_bits(host, values):
+    with pytest.raises(ValueError, match="parent"):
+        host.kvq._int32s(values, "parent")
+    assert host.kvq._int32s([-2 ** 31, 0, 2 ** 31 - 1], "parent")[:] == [-2 ** 31, 0, 2 ** 31 - 1]
 
 
 @pytest.mark.parametrize("dt", [0, 2])

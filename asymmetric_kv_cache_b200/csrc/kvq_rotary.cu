@@ -28,6 +28,9 @@ namespace kvq {
 namespace {
 
 constexpr int kRotThreads = 256;
+// rows of a block (32 KB of them on their way; a block for each row of few)
+template <int DT>
+constexpr int kRotRows = DT == KVQ_FP32 ? 4 : 8;
 
 // A lane's two pieces of four values as they are in memory, and as fp32.
 template <int DT>
@@ -44,6 +47,11 @@ __device__ __forceinline__ void load8(const unsigned char* p0, const unsigned ch
     const uint2 a = *reinterpret_cast<const uint2*>(p0), b = *reinterpret_cast<const uint2*>(p1);
     r.v[0] = a.x; r.v[1] = a.y; r.v[2] = b.x; r.v[3] = b.y;
   }
+}
+// A piece on its way into shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_piece(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
 template <int DT>
 __device__ __forceinline__ void unpack8(const Raw8<DT>& r, float (&y)[8]) {
@@ -88,32 +96,36 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = t;
 }
 
-// Grid: x = rows, NG groups of RB to a block; y = slices of the heads (a block
-// takes the passes slice, slice + gridDim.y, .. of kRotThreads / (D / 8) head
-// rows).
+// Grid: x = rows, ROWS to a block; y = slices of the heads (a block takes the
+// passes slice, slice + gridDim.y, .. of kRotThreads / (D / 8) head rows).
 //
 // The block's rows share one round of angles.  A thread keeps its head through
-// them (pointers step, the weight stays in registers) and has the next RB
-// loads under way.  16000 rows of 32 + 8 + 8 heads of 128, bf16 to fp16 (393
-// MB), us: one row to a block 158; four, the partner by shuffles, 119; pairs in
-// a lane 113; 8 rows to a block, two at a time, in 64 registers and so four
-// blocks on an SM, 109; a head through all 8 rows 103 (94 without the norms):
-// 3.8 TB/s, 0.58 of the measured copy.  Issue and the loads' latency bound it
-// together; prefetching the block's rows into the second-level cache made it
-// 119.
-template <int D, int IN, int OUT, int RB, int NG>
+// them (the weight stays in registers).  Its pieces of all the rows are copied
+// into shared memory ahead of their use, each replaced by that of the next
+// pass when it is read; a thread reads only what it copied itself, so nothing
+// but its own copies is waited for.  16000 rows of 32 + 8 + 8 heads of 128,
+// bf16 to fp16 (393 MB), us: one row to a block, from memory into registers,
+// 158; four rows, the partner by shuffles, 119; pairs in a lane 113; 8 rows, a
+// head through all of them, the next two rows' loads under way, 103; with the
+// copies 72 (65 without the norms): 5.4 TB/s, 0.83 of the measured copy.  The
+// time between load and use had bound it, not issue: packed fp32 arithmetic
+// left it at 74, five blocks on an SM (48 registers) made it 90, two rows
+// unrolled 74.
+template <int D, int IN, int OUT, int ROWS>
 __global__ void __launch_bounds__(kRotThreads, 4)
     norm_rotary_kernel(const RotaryArgs a, const RotarySeqs seqs, int rows) {
   constexpr int LPH = D / 8;                   // lanes of a head row
   constexpr int HPB = kRotThreads / LPH;       // head rows of one pass of the block
   constexpr int64_t IS = IN == KVQ_FP32 ? 4 : 2, OS = OUT == KVQ_FP32 ? 4 : 2;
-  __shared__ float4 cs[RB * NG][D / 8], sn[RB * NG][D / 8];
+  constexpr int PIECE = 4 * IS;
+  __shared__ __align__(16) unsigned char slots[ROWS][2][kRotThreads * PIECE];
+  __shared__ float4 cs[ROWS][D / 8], sn[ROWS][D / 8];
   __shared__ float stage[kRotThreads * 8];
   const int tid = threadIdx.x, l = tid % LPH, hl = tid / LPH;
-  const int b0 = blockIdx.x * (RB * NG);       // the block's first row, of the launch
+  const int b0 = blockIdx.x * ROWS;            // the block's first row, of the launch
   const int64_t row0 = seqs.row0 + b0;
   const int P = a.n_pairs;
-  const int all = min(RB * NG, rows - b0);
+  const int all = min(ROWS, rows - b0);
   const int heads = a.hq + a.hkv + (a.v ? a.hkv : 0);
   // this lane's pieces: channels o0 .. and o1 ..; of them pairs 4 l .. rotated
   const bool apart = !a.interleaved && P % 4 == 0, staged = !a.interleaved && P % 4 != 0;
@@ -142,15 +154,16 @@ __global__ void __launch_bounds__(kRotThreads, 4)
     x.dst = reinterpret_cast<unsigned char*>(dst) + row0 * x.dst_step + h * D * OS;
     return x;
   };
-  auto load = [&](const Head& x, int g0, Raw8<IN> (&raw)[RB]) {
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-      if (x.part < 3 && g0 + r < all)
-        load8<IN>(x.src + (g0 + r) * x.src_step + o0 * IS, x.src + (g0 + r) * x.src_step + o1 * IS, raw[r]);
+  auto fetch = [&](const Head& x, int r) {
+    if (x.part < 3 && r < all) {
+      copy_piece<PIECE>(slots[r][0] + tid * PIECE, x.src + r * x.src_step + o0 * IS);
+      copy_piece<PIECE>(slots[r][1] + tid * PIECE, x.src + r * x.src_step + o1 * IS);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  Raw8<IN> next[RB];
   Head ahead = head_of(blockIdx.y * HPB);
-  load(ahead, 0, next);
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) fetch(ahead, r);
 
   for (int i = tid; i < all * P; i += kRotThreads) {
     const int r = i / P, pair = i % P, line = b0 + r;
@@ -185,21 +198,17 @@ __global__ void __launch_bounds__(kRotThreads, 4)
       unpack8<IN>(wr, wv);
     }
     const bool norm = __any_sync(0xffffffffu, w != nullptr), line_up = staged && __any_sync(0xffffffffu, x.part < 2);
+    ahead.part = 3;
+    if (h0 + (int)gridDim.y * HPB < heads) ahead = head_of(h0 + gridDim.y * HPB);
 #pragma unroll 1
-    for (int g0 = 0; g0 < all; g0 += RB) {
-      const int nr = min(RB, all - g0);
-      Raw8<IN> raw[RB];
-#pragma unroll
-      for (int r = 0; r < RB; ++r) raw[r] = next[r];
-      if (g0 + RB < all) {
-        load(x, g0 + RB, next);
-      } else if (h0 + (int)gridDim.y * HPB < heads) {
-        ahead = head_of(h0 + gridDim.y * HPB);
-        load(ahead, 0, next);
-      }
-      auto work = [&](int r) {
+    for (int r = 0; r < ROWS; ++r) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(ROWS - 1) : "memory");
+      Raw8<IN> raw;
+      load8<IN>(slots[r][0] + tid * PIECE, slots[r][1] + tid * PIECE, raw);
+      fetch(ahead, r);
+      if (r < all) {
         float y[8];
-        unpack8<IN>(raw[r], y);
+        unpack8<IN>(raw, y);
         if (norm) {
           float ss = 0.f;
 #pragma unroll
@@ -214,8 +223,8 @@ __global__ void __launch_bounds__(kRotThreads, 4)
         }
         if (line_up) {
           float* row = stage + (tid - l) * 8;      // the head row, written and read by its own lanes
-          const float* c = reinterpret_cast<const float*>(cs[g0 + r]);
-          const float* s = reinterpret_cast<const float*>(sn[g0 + r]);
+          const float* c = reinterpret_cast<const float*>(cs[r]);
+          const float* s = reinterpret_cast<const float*>(sn[r]);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) row[8 * l + i] = y[i];
@@ -227,7 +236,7 @@ __global__ void __launch_bounds__(kRotThreads, 4)
             else if (x.part < 2 && e < 2 * P) y[i] = fmaf(row[e - P], s[e - P], y[i] * c[e - P]);
           }
         } else if (x.part < 2 && pairs > 0) {
-          const float4 c4 = cs[g0 + r][l], s4 = sn[g0 + r][l];
+          const float4 c4 = cs[r][l], s4 = sn[r][l];
           const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
           if (apart) {
 #pragma unroll
@@ -239,15 +248,7 @@ __global__ void __launch_bounds__(kRotThreads, 4)
           }
         }
         if (x.part < 3)
-          store8<OUT>(x.dst + (g0 + r) * x.dst_step + o0 * OS, x.dst + (g0 + r) * x.dst_step + o1 * OS, y);
-      };
-      if (nr == RB) {
-#pragma unroll
-        for (int r = 0; r < RB; ++r) work(r);
-      } else {
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-          if (r < nr) work(r);
+          store8<OUT>(x.dst + r * x.dst_step + o0 * OS, x.dst + r * x.dst_step + o1 * OS, y);
       }
     }
   }
@@ -260,17 +261,21 @@ cudaError_t launch_norm_rotary(int d, int dtype, int out_dtype, const RotaryArgs
   const int hpb = kRotThreads / (d / 8);
   const int heads = a.hq + a.hkv + (a.v ? a.hkv : 0);
   const int passes = (heads + hpb - 1) / hpb;
-  // few rows: a row and a pass to a block, so that their latencies overlap
-  const bool few = rows < 1024;
+  // A block for each row and pass as long as blocks of several rows would leave
+  // SMs idle: their latencies overlap.  32 + 8 + 8 heads of 128, one / several
+  // rows to a block, us: bf16, 8 rows a block, 64 rows 2.5 / 11.2, 512 6.6 /
+  // 11.5, 1020 11.3 / 11.7; fp32, 4 rows a block, 512 6.7 / 7.3, 768 9.0 / 8.6.
+  const bool few = rows < 148 * (dtype == KVQ_FP32 ? kRotRows<KVQ_FP32> : kRotRows<KVQ_FP16>);
   const int slices = few ? (passes < 64 ? passes : 64) : 1;
 #define KVQ_ROTARY_CASE(D_, I_, O_)                                                       \
   if (d == D_ && dtype == I_ && out_dtype == O_) {                                        \
     if (few)                                                                              \
-      norm_rotary_kernel<D_, I_, O_, 1, 1><<<dim3((unsigned)rows, (unsigned)slices),      \
-                                             kRotThreads, 0, stream>>>(a, seqs, rows);    \
+      norm_rotary_kernel<D_, I_, O_, 1><<<dim3((unsigned)rows, (unsigned)slices),         \
+                                          kRotThreads, 0, stream>>>(a, seqs, rows);       \
     else                                                                                  \
-      norm_rotary_kernel<D_, I_, O_, 2, 4><<<(unsigned)((rows + 7) / 8), kRotThreads, 0,  \
-                                             stream>>>(a, seqs, rows);                    \
+      norm_rotary_kernel<D_, I_, O_, kRotRows<I_>>                                        \
+          <<<(unsigned)((rows - 1) / kRotRows<I_> + 1), kRotThreads, 0, stream>>>(        \
+              a, seqs, rows);                                                             \
     return cudaGetLastError();                                                            \
   }
 #define KVQ_ROTARY_OUT(D_, I_) \

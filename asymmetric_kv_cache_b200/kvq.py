@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -51,11 +52,11 @@ class KvqLayout(ctypes.Structure):
 
 
 def _int32s(values, name: str):
-    """A C array of integers that fit (ctypes would cut off the upper bits of others)."""
-    arr = (ctypes.c_int32 * len(values))(*values)
-    if arr[:] != list(values):
-        raise ValueError(f"{name} must be 32-bit integers")
-    return arr
+    """The integers as an array of int32 (ctypes would cut off the upper bits of those that do not fit)."""
+    try:
+        return array("i", values)
+    except OverflowError:
+        raise ValueError(f"{name} must be 32-bit integers") from None
 
 
 class KvqScores(ctypes.Structure):
@@ -95,13 +96,13 @@ kvq_append = _sig("kvq_append", [_vp, _vp, _vp, ctypes.c_int32, _P(ctypes.c_int3
                                  ctypes.c_int32, _vp])
 kvq_decode = _sig("kvq_decode", [_vp, _vp, ctypes.c_int32, _vp, ctypes.c_int32, _vp,
                                  ctypes.c_size_t, _vp])
-kvq_attend = _sig("kvq_attend", [_vp, _vp, ctypes.c_int32, _P(ctypes.c_int32), ctypes.c_int32,
+kvq_attend = _sig("kvq_attend", [_vp, _vp, ctypes.c_int32, _vp, ctypes.c_int32,
                                  _P(KvqScores), _vp, _vp, ctypes.c_size_t, _vp])
 kvq_norm_rotary = _sig("kvq_norm_rotary",
                        [_vp, _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp, ctypes.c_int64,
-                        ctypes.c_int32, _P(ctypes.c_int32), ctypes.c_int32, _P(KvqRotary), _vp, _vp,
-                        _vp, ctypes.c_int32, _vp])
-kvq_reorder = _sig("kvq_reorder", [_vp, _P(ctypes.c_int32), ctypes.c_int32, ctypes.c_int32, _vp])
+                        ctypes.c_int32, _vp, ctypes.c_int32, _P(KvqRotary), _vp, _vp, _vp,
+                        ctypes.c_int32, _vp])
+kvq_reorder = _sig("kvq_reorder", [_vp, _vp, ctypes.c_int32, ctypes.c_int32, _vp])
 kvq_workspace_init = _sig("kvq_workspace_init", [_vp, ctypes.c_size_t, _vp])
 kvq_workspace_status = _sig("kvq_workspace_status", [_vp, _vp])
 kvq_cache_config = _sig("kvq_cache_config", [_vp, _P(KvqConfig)])
@@ -318,16 +319,18 @@ class KVQCache:
         dt = DTYPE_CODES.get(q.dtype)
         if dt is None:
             raise ValueError("q must be fp16, bf16 or fp32")
+        if not -2 ** 31 <= window < 2 ** 31:
+            raise ValueError("window must be a 32-bit integer")
         sp, n_seq = self.spec, len(n_q)
         arr = _int32s(n_q, "n_q")
         shape = (sum(n_q), sp.n_q_heads, sp.head_dim)
         qp = self._ptr(q, "q", None, shape)
-        sc = KvqScores(scale, cap, _int32s((window,), "window")[0],
+        sc = KvqScores(scale, cap, window,
                        None if slopes is None else self._ptr(slopes, "slopes", torch.float32, (sp.n_q_heads,)),
                        None if prefix is None else self._ptr(prefix, "prefix", torch.int32, (n_seq,)))
         if out is None:
             out = torch.empty(shape, dtype=torch.float16, device=q.device)
-        self._launch("kvq_attend", kvq_attend, stream, self._h, qp, dt, arr, n_seq, ctypes.byref(sc),
+        self._launch("kvq_attend", kvq_attend, stream, self._h, qp, dt, arr.buffer_info()[0], n_seq, ctypes.byref(sc),
                      self._ptr(out, "out", torch.float16, shape), self.workspace.data_ptr(),
                      self.workspace.numel())
         return out
@@ -382,7 +385,7 @@ class KVQCache:
                 raise ValueError(f"sections must give the pairs of {axes} axes")
             rot.positions = self._ptr(positions, "positions", torch.int32)
             rot.n_axes = axes
-            rot.sections[:axes] = _int32s(sections, "sections")[:]
+            rot.sections[:axes] = _int32s(sections, "sections")[:axes]
         elif sections is not None:
             raise ValueError("sections go with positions")
         if out is None:
@@ -392,8 +395,8 @@ class KVQCache:
         qo, ko, vo = out
         if qo is None or ko is None or (vo is None) != (v is None):
             raise ValueError("out must hold a tensor for each of q, k and v")
-        self._launch("kvq_norm_rotary", kvq_norm_rotary, stream, self._h, qp, qs, kp, ks, vp, vs, dt, arr, n_seq,
-                     ctypes.byref(rot), self._ptr(qo, "q output", out_dtype, q_shape),
+        self._launch("kvq_norm_rotary", kvq_norm_rotary, stream, self._h, qp, qs, kp, ks, vp, vs, dt,
+                     arr.buffer_info()[0], n_seq, ctypes.byref(rot), self._ptr(qo, "q output", out_dtype, q_shape),
                      self._ptr(ko, "k output", out_dtype, k_shape),
                      None if vo is None else self._ptr(vo, "v output", out_dtype, k_shape), odt)
         return qo, ko, vo
@@ -401,8 +404,10 @@ class KVQCache:
     def reorder(self, parent, shared: int = 0, stream=None):
         """Sequence b takes over sequence ``parent[b]``, all at once (kvq_reorder); the first
         ``shared`` tokens of moving sequences and their parents are the same already."""
-        self._launch("kvq_reorder", kvq_reorder, stream, self._h, _int32s(parent, "parent"), len(parent),
-                     _int32s((shared,), "shared")[0])
+        if not -2 ** 31 <= shared < 2 ** 31:
+            raise ValueError("shared must be a 32-bit integer")
+        arr = _int32s(parent, "parent")
+        self._launch("kvq_reorder", kvq_reorder, stream, self._h, arr.buffer_info()[0], len(arr), int(shared))
 
     def workspace_status(self, stream=None) -> int:
         return kvq_workspace_status(self.workspace.data_ptr(), _stream(stream))

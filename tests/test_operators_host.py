@@ -69,7 +69,7 @@ def test_out_beside_q(host):
 def test_integers_keep_their_upper_bits(host, values):
     with pytest.raises(ValueError, match="parent"):
         host.kvq._int32s(values, "parent")
-    assert host.kvq._int32s([-2 ** 31, 0, 2 ** 31 - 1], "parent")[:] == [-2 ** 31, 0, 2 ** 31 - 1]
+    assert list(host.kvq._int32s([-2 ** 31, 0, 2 ** 31 - 1], "parent")) == [-2 ** 31, 0, 2 ** 31 - 1]
 
 
 @pytest.mark.parametrize("dt", [0, 2])

@@ -46,11 +46,12 @@ __device__ __forceinline__ void move_units(const Geom& g, unsigned char* at, int
   uint32_t live = 0;
 #pragma unroll
   for (int k = 0; k < NB; ++k) {
-    const MoveArea m = mv[k];               // (entries from n on are empty)
+    const MoveArea m = mv[k];
+    const uint32_t hi = k < n ? m.hi : 0u;
 #pragma unroll
     for (int x = 0; x < UN; ++x) {
       const uint32_t uu = u + x * kReorderThreads;
-      bool on = uu >= m.lo && uu < m.hi;
+      bool on = uu >= m.lo && uu < hi;
       if (AK && blocks && on) {
         const uint32_t upb = g.block_bytes / 16;
         const int grp = lo_group + (int)(uu / upb);
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kReorderThreads, NB == 8 ? 3 : 4)
     reorder_kernel(const Geom g, unsigned char* cache, const ReorderMoves mv, int32_t shared_tokens) {
   constexpr int kUnits = 8 / NB, kReorderTile = kReorderThreads * kUnits;
   __shared__ int32_t s_len[kReorderMoves], d_len[kReorderMoves];
-  __shared__ MoveArea area_of[kReorderBatch];
+  __shared__ MoveArea area_of[3][kReorderMoves + kReorderBatch];   // (entries behind a batch are read, not used)
   __shared__ int32_t range[2], last;
   const int tid = threadIdx.x;
   const int m0 = mv.chain_start[blockIdx.y], m1 = mv.chain_start[blockIdx.y + 1];
@@ -119,6 +120,17 @@ __global__ void __launch_bounds__(kReorderThreads, NB == 8 ? 3 : 4)
                 st = (sink_units + kReorderTile - 1) / kReorderTile;
   const int64_t per_head = bt + tt + st;
 
+  // every move's units of each area, once for all tiles: the tiles' loop has no
+  // barrier (with a batch's entries set up for each tile between two barriers
+  // 12 moves of 8100 tokens, 100 MB, took 47.4 us instead of 44.9)
+  for (int m = tid; m < m1 - m0; m += kReorderThreads) {
+    const int sn = s_len[m], dn = d_len[m], src = mv.src[m0 + m], dst = mv.dst[m0 + m];
+    area_of[0][m] = MoveArea{src, dst, (uint32_t)(kept(sn, dn) - lo_group) * upb, (uint32_t)(groups(sn) - lo_group) * upb};
+    area_of[1][m] = MoveArea{src, dst, 0u, sn == 0 ? 0u : (uint32_t)tail_units};
+    area_of[2][m] = MoveArea{src, dst, 0u, sn == 0 ? 0u : (uint32_t)sink_units};
+  }
+  __syncthreads();
+
   for (int64_t tile = blockIdx.x; tile < per_head * g.hkv; tile += gridDim.x) {
     const int h = (int)(tile / per_head);
     int64_t t = tile % per_head;
@@ -131,26 +143,12 @@ __global__ void __launch_bounds__(kReorderThreads, NB == 8 ? 3 : 4)
     unsigned char* at = cache + (area == 0 ? g.blocks_off + (int64_t)lo_group * g.block_bytes
                                  : area == 1 ? g.tails_off
                                              : g.sinks_off) + h * per_seq;
-    for (int m = m0; m < m1;) {
-      // the batch: consecutive moves with the same number
-      int n = 1;
-      while (m + n < m1 && mv.batch[m + n] == mv.batch[m]) ++n;
-      __syncthreads();
-      if (tid >= n && tid < NB) area_of[tid] = MoveArea{0, 0, 0u, 0u};
-      if (tid < n) {
-        const int sn = s_len[m + tid - m0], dn = d_len[m + tid - m0];
-        MoveArea a;
-        a.src = mv.src[m + tid];
-        a.dst = mv.dst[m + tid];
-        a.lo = area == 0 ? (uint32_t)(kept(sn, dn) - lo_group) * upb : 0u;
-        a.hi = area == 0 ? (uint32_t)(groups(sn) - lo_group) * upb
-                         : sn == 0 ? 0u : (uint32_t)(area == 1 ? tail_units : sink_units);
-        area_of[tid] = a;
-      }
-      __syncthreads();
-      const int32_t* len = s_len + (m - m0);
-      move_units<NB, kUnits, AK>(g, at, per_seq * g.hkv, area_of, len, u0, n, area == 0, lo_group);
-      m += n;
+    // the batches, consecutive moves with the same number
+#pragma unroll 1
+    for (int m = m0, n; m < m1; m += n) {
+#pragma unroll 1
+      for (n = 1; m + n < m1 && mv.batch[m + n] == mv.batch[m];) ++n;
+      move_units<NB, kUnits, AK>(g, at, per_seq * g.hkv, area_of[area] + (m - m0), s_len + (m - m0), u0, n, area == 0, lo_group);
     }
   }
 

@@ -609,8 +609,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           upk2(fma2(pk2(s[i], s[i + 1]), mul_2, base_2), p0, p1);
           p0 = fast_exp2(p0);
           p1 = fast_exp2(p1);
-          sum[i / 2 & 1] = add2(sum[i / 2 & 1], pk2(p0, p1));
+          // the sum is of the weights as rounded: where few keys carry the row,
+          // their rounding cancels (the six turns' error against float64, as a
+          // 2-norm, 3.0e-4 -> 2.8e-4, for 1.5 % of the time)
           p[i / 2] = pack_h2(p0, p1);
+          const float2 f = __half22float2(u32_as_h2(p[i / 2]));
+          sum[i / 2 & 1] = add2(sum[i / 2 & 1], pk2(f.x, f.y));
         }
         {
           float x, y;

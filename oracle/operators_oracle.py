@@ -55,7 +55,8 @@ def attend(cfg: o.Config, k16, v16, q, scale: float = 0.0, cap: float = 0.0, win
 
     tol per element, with A = sum_j alpha_j |v_j|, all roundings at most half a step (fp16: 2^-11 relative):
       2^-11 |out|     the result's rounding
-      2^-11 A         the weights' rounding to fp16
+      2^-11 (A + |out|) the weights' rounding to fp16, p_j (1 + d_j) with |d_j| <= 2^-11: where the sum is of the rounded weights
+                      too, the result is off by sum_j alpha_j d_j (v_j - out), and sum_j alpha_j |v_j - out| <= A + |out|
       2^-11 A         the values' (s code + z) rounding to fp16
       n 2^-25 max|v|  weights below 2^-14 of the largest are subnormal in fp16: off by 2^-25 at most
       2 delta A       scores off by delta move the result by at most 2 delta A
@@ -88,7 +89,7 @@ def attend(cfg: o.Config, k16, v16, q, scale: float = 0.0, cap: float = 0.0, win
     mass = (np.abs(q) * kk[0]).sum(-1)                                           # [n_q, Hq]
     big = np.where(seen & (alpha > 1e-9), np.abs(s), 0.0).max(-1).T + cap
     delta = scale * (2.0 ** -17 * mass + d * 15 * 2.0 ** -25) + 2.0 ** -20 * (1 + big)
-    tol = 2.0 ** -11 * (np.abs(out) + 2 * A) + n * 2.0 ** -25 * np.abs(vh).max() + 2 * delta[..., None] * A + 2.0 ** -24
+    tol = 2.0 ** -11 * 2 * (np.abs(out) + A) + n * 2.0 ** -25 * np.abs(vh).max() + 2 * delta[..., None] * A + 2.0 ** -24
     if cfg.rotate:
         tol = np.sqrt((tol ** 2).sum(-1, keepdims=True)) + 2.0 ** -11 * np.abs(out).max(-1, keepdims=True)
         tol = np.broadcast_to(tol, out.shape) + 2.0 ** -21 * np.linalg.norm(out, axis=-1, keepdims=True)

@@ -19,9 +19,11 @@
 //     fp16 value plus its exact residual (one fused multiply-subtract), rows
 //     0-7 of the 16-row A operand holding the one and rows 8-15 the other,
 //     so the logits carry ~22 bits at no extra tile.
-//   * p goes to fp16 (one rounding, relative 2^-11 at most), v = s code + z
-//     to fp16 (one fused rounding).  With at most 4 rows, columns 4-7 of the
-//     value product are free and carry p's residual: p is then exact to 2^-22.
+//   * p goes to fp16 (one rounding, relative 2^-11 at most, and the sum is of
+//     the rounded weights, so that it cancels where few keys carry a row), v =
+//     s code + z to fp16 (one fused rounding).  With at most 4 rows, columns 4-7
+//     of the value product are free and carry p's residual: p is then exact to
+//     2^-22.
 //   * all sums, maxima and the two accumulators are fp32.
 #pragma once
 
@@ -251,12 +253,12 @@ __device__ __forceinline__ void att_softmax(AttState<MT>& st, float (&s)[NT][2],
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float p0 = fast_exp2(s[nt][0] - base), p1 = fast_exp2(s[nt][1] - base);
-    st.l += p0 + p1;
     uint32_t h = pack_h2(p0, p1);
-    if (low) {
-      const float2 f = __half22float2(u32_as_h2(h));
-      h = pack_h2(p0 - f.x, p1 - f.y);
-    }
+    const float2 f = __half22float2(u32_as_h2(h));
+    // the sum is of the weights that the values meet: with a residual both
+    // parts, else the rounded ones (a row whose values are alike is their value)
+    st.l += dup ? p0 + p1 : f.x + f.y;
+    if (low) h = pack_h2(p0 - f.x, p1 - f.y);
     pb[nt] = h;
   }
 }

@@ -285,3 +285,24 @@ def test_python_refusals():
     for bad in (lambda: cache.attend(q, [2], cap=-1.0), lambda: cache.attend(q, [1, 1]), lambda: cache.attend(q, [2], window=-3)):
         with pytest.raises(K.KvqError):
             bad()
+
+
+@pytest.mark.parametrize("gqa,n_q,R", [(8, 1, 0), (4, 5, 0), (8, 40, 64), (2, 1, 32)])
+def test_values_all_alike(gqa, n_q, R):
+    """Rows whose values are all the number 2040 / 1024 are that number: the weights that the values meet and the weights that
+    they are divided by are the same ones, as rounded.  (fp16 steps by 2^-10 there: a sum that is off by 2^-12 of itself moves
+    the result; fp32 sums of the 700 same weights are off by 700 2^-24 = 2^-14.5 at most.)"""
+    hkv, d, lens = 2, 128, [700, 70, 45]
+    spec = tl.kvq().CacheSpec(4, 4, 32, d, hkv * gqa, hkv, 3, 1024, window=R)
+    rng = np.random.default_rng(gqa + n_q)
+    ks, vs = _hist(rng, lens, hkv, d)
+    for k, v in zip(ks, vs):
+        # one key takes weight 1, the others some weight between 0 and 1, the same for all of them
+        k[:] = k[:1]
+        k[len(k) // 2] = k[0] + rng.standard_normal(k[0].shape).astype(np.float16)
+        v[:] = 2040 / 1024
+    counts = [min(n, n_q) for n in lens]
+    cache = _filled(spec, ks, vs)
+    for _ in range(4):
+        out = cache.attend(tl.to_device(_queries(rng, counts, hkv * gqa, d, "fp16"), "fp16"), counts)
+        assert (out == 2040 / 1024).all(), (out != 2040 / 1024).float().mean().item()

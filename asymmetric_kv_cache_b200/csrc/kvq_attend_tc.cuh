@@ -228,6 +228,13 @@ __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, 
   lds_words<WV>(word(OFF_V + (kv * 32 + lane) * (4 * WV)), vw);
   lds_words<2 * J>(word(OFF_VS + (4 * kv + i4) * J * 8), vs);
   lds_words<2 * J>(word(OFF_VZ + (4 * kv + i4) * J * 8), vz);
+  // From the scales 4368 and 21840 on (bits below; scales are not negative) 15
+  // and 3 steps round to infinity in fp16.  A lane looks at its part of all.
+  constexpr uint32_t kWide = 0x8000u - (KBL == 4 ? 0x6C44u : 0x7555u);
+  uint32_t sw[D / 64], wide = 0;
+  lds_words<D / 64>(word(OFF_S) + lane * (D / 64), sw);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) wide |= sw[i] + (kWide | kWide << 16);   // bit 15: at least that scale
   wait();
   // this lane's row of its matrix of four: neighbouring channel eights for the
   // keys, (channel eight, token eight) for the values
@@ -262,6 +269,33 @@ __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, 
     });
     stmatrix4(v1 + 2 * mt * (kTcKeys / 8) * 128, o[0], o[1], o[2], o[3]);
   });
+  // A channel whose keys spread over more than 65504: s code was infinite above
+  // though s code + z is not.  The block's keys are written again from fp32,
+  // whose products are exact and whose sums are off by 2^-24 (a short loop over
+  // the words in shared memory, hardly ever run; as a branch around the fp16
+  // form it kept that from being mixed with the values' and cost six turns 4 %).
+  if (__any_sync(0xffffffffu, wide & 0x80008000u)) {
+#pragma unroll 1
+    for (int i = 0; i < P / 2; ++i) {
+      const int pc = i >> 1, x = i & 1;
+      const uint32_t w = word(((2 * kv + x) * 32 + lane) * LBK)[4 * pc / FK] >> (4 * pc % FK * 2);
+      uint32_t s4[4], z4[4], hi[4], lo[4];
+      lds_words<4>(word(OFF_S + i4 * (D / 2)) + 4 * pc, s4);
+      lds_words<4>(word(OFF_Z + i4 * (D / 2)) + 4 * pc, z4);
+      static_for<4>([&](auto qc) {
+        constexpr int q = decltype(qc)::value;
+        const float2 c = __half22float2(u32_as_h2(unpack_pair<KBL, q>(w))), sc = __half22float2(u32_as_h2(s4[q])),
+                     z = __half22float2(u32_as_h2(z4[q]));
+        const float y0 = fmaf(c.x, sc.x, z.x), y1 = fmaf(c.y, sc.y, z.y);
+        hi[q] = pack_h2(y0, y1);
+        const float2 f = __half22float2(u32_as_h2(hi[q]));
+        lo[q] = pack_h2(y0 - f.x, y1 - f.y);
+      });
+      const uint32_t at = k1 + (x * P + 4 * pc) * 128;
+      stmatrix4(at, hi[0], hi[1], hi[2], hi[3]);
+      stmatrix4(at + (kTcKeys * D * 2), lo[0], lo[1], lo[2], lo[3]);
+    }
+  }
 }
 
 // The same for 16 fp16 tokens, `valid` of which hold tokens (0 for a part

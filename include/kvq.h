@@ -361,6 +361,8 @@ typedef struct {
  * call may be replayed as appends advance them; out is then of the newest
  * tokens at that time.  The cache's contents must be finite (as the append's
  * are): an infinity or NaN in a key or value may reach rows that do not see it.
+ * Keys and values of magnitude up to 65440 are read as finite numbers; beyond,
+ * the fp16 scale of their group, rounded up, may take the largest past 65504.
  * A call runs on register tiles, on the tensor cores (many rows per kv head
  * and many keys) or, sequence by sequence, on both.  The environment variable
  * KVQ_ATTEND_TC, if set to 0 or 1, has the one or the other take every

@@ -306,3 +306,33 @@ def test_values_all_alike(gqa, n_q, R):
     for _ in range(4):
         out = cache.attend(tl.to_device(_queries(rng, counts, hkv * gqa, d, "fp16"), "fp16"), counts)
         assert (out == 2040 / 1024).all(), (out != 2040 / 1024).float().mean().item()
+
+
+def _wide(rng, lens, hkv, d, most):
+    """Histories of which every third channel's keys and every fifth's values reach over most to -most in every group."""
+    ks, vs = _hist(rng, lens, hkv, d)
+    for x, step in ((ks, 3), (vs, 5)):
+        for h in x:
+            h[:, :, ::step] = rng.uniform(-most, most, h[:, :, ::step].shape).astype(np.float16)
+            h[::7, :, ::step], h[3::7, :, ::step] = most, -most
+    return ks, vs
+
+
+@pytest.mark.parametrize("d,G", [(128, 32), (64, 64)])
+@pytest.mark.parametrize("kb,vb,delta", [(4, 2, 0), (2, 4, 0), (4, 4, 64)])
+@pytest.mark.parametrize("most", [40000, 65440])
+def test_keys_and_values_over_all_of_fp16(kb, vb, delta, d, G, most):
+    """Groups whose keys or values spread over more than 65504: 15 steps of the scale are no fp16 number then, the keys are."""
+    hkv, gqa = 2, 4
+    lens, n_q = [5 * G + 9, 9 * G, 40], [50, 1, 7]
+    kw = dict(akvq_delta=delta) if delta else dict(window=16, sink=5)
+    spec = tl.kvq().CacheSpec(kb, vb, G, d, hkv * gqa, hkv, 3, 1024, **kw)
+    rng = np.random.default_rng(kb * 10 + vb + d + most)
+    ks, vs = _wide(rng, lens, hkv, d, most)
+    q = _queries(rng, n_q, hkv * gqa, d, "fp16") * 0.25
+    cache = _filled(spec, ks, vs)
+    for x in (dict(scale=2e-5), dict(scale=2e-5, cap=3.0, window=100)):
+        for b in range(3):                      # (an adaptive cache's bytes are those of its own append)
+            m = [n if i == b else 0 for i, n in enumerate(n_q)]
+            part = q[sum(n_q[:b]):sum(n_q[:b + 1])]
+            _check(cache, spec, ks, vs, part, m, chunks=[lens[b]] if delta else None, **x)

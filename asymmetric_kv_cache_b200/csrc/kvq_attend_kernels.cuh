@@ -66,15 +66,17 @@ struct RowRule {
   float cap2, inv_cap;       // cap * log2(e) and scale / cap; 0 when there is none
   float slope2;              // slope * log2(e)
 };
+// mul: what the row's query was divided by.
 __device__ __forceinline__ RowRule att_rule(const AttendArgs& a, int pos, int prefix, int window,
-                                            int head) {
+                                            int head, float mul = 1.f) {
+  constexpr float kMax = 3.402823466e38f;      // (infinite, they would turn a product of 0 into NaN)
   RowRule rr;
   rr.pos = pos;
   rr.prefix = prefix;
   rr.window = window;
-  rr.scale2 = a.scale * kLog2e;
+  rr.scale2 = fminf(a.scale * kLog2e * mul, kMax);
   rr.cap2 = a.cap * kLog2e;
-  rr.inv_cap = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  rr.inv_cap = a.cap > 0.f ? fminf(a.scale / a.cap * mul, kMax) : 0.f;
   rr.slope2 = a.slopes ? a.slopes[head] * kLog2e : 0.f;
   return rr;
 }
@@ -508,6 +510,13 @@ __global__ void __launch_bounds__(kAttThreads, 4)
   // ---- query rows: rotated where the cache is, value and residual parts in
   // fragment order.  Warp w takes rows 2w and 2w + 1; row r >= nr is zero,
   // but with at most 4 rows the upper 4 repeat the lower ones.
+  // A query is multiplied by the blocks' key scales in fp16, and those reach
+  // 8736 (4 bits) and 43680 (2 bits): a row with values from 4 and 1 on is
+  // divided by a power of two, which its scores' scale takes back.  (Rows below
+  // that are left as they are: in a division a residual may lose its last bits,
+  // 2^-25 of the divided row.)
+  __shared__ float row_mul[kAttendRows];
+  const int room = KB == 4 && !g.akvq_delta ? 2 : 0;     // log2 of the largest value that is left
   {
     constexpr int V = D / 32;
 #pragma unroll
@@ -526,6 +535,18 @@ __global__ void __launch_bounds__(kAttThreads, 4)
 #pragma unroll
         for (int i = 0; i < V; ++i) y[i] *= rot_scale<D>();
       }
+      float mul = 1.f, big = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) big = fmaxf(big, fabsf(y[i]));
+      if (__any_sync(0xffffffffu, big >= (float)(1 << room))) {
+        // (the bits of numbers that are not negative order as the numbers do)
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+        const int e = min((int)(top >> 23) - 126 - room, 16);     // y 2^-e is below 2^room
+        mul = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] *= __uint_as_float((uint32_t)(127 - e) << 23);
+      }
+      if (lane == 0) row_mul[r] = mul;
 #pragma unroll
       for (int i = 0; i < V; i += 2) {
         const uint32_t hi = pack_h2(y[i], y[i + 1]);
@@ -541,7 +562,7 @@ __global__ void __launch_bounds__(kAttThreads, 4)
   __syncthreads();
 
   const int rc = min(dup ? g8 & 3 : g8, nr - 1);
-  const RowRule rr = att_rule(a, n - nq + (r0 + rc) / g.gqa, prefix, window, h * g.gqa + (r0 + rc) % g.gqa);
+  const RowRule rr = att_rule(a, n - nq + (r0 + rc) / g.gqa, prefix, window, h * g.gqa + (r0 + rc) % g.gqa, row_mul[rc]);
   AttState<C::MT> st;
 #pragma unroll
   for (int mt = 0; mt < C::MT; ++mt) st.o[mt][0] = st.o[mt][1] = st.o[mt][2] = st.o[mt][3] = 0.f;

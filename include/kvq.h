@@ -351,9 +351,11 @@ typedef struct {
  * q: device [sum_b n_q[b], n_q_heads, d], sequences concatenated in order b
  * (fp16, bf16 or fp32, 16-byte aligned), read only; out: device, the same
  * shape, fp16, written, not overlapping q.  The kernels hold a query in fp16
- * (fp32 and rotated ones as a value and its residual): magnitudes above 65504
- * become infinite, bf16 ones below 2^-14 are held to 2^-25.  n_q: host array of n_seq counts, each at most the
- * sequence's length (0 skips the sequence), read before the call returns;
+ * (fp32 and rotated ones as a value and its residual; rows of large values may
+ * be held divided by a power of two): magnitudes above 65504 may become
+ * infinite, bf16 ones below 2^-14 are held to 2^-25.  n_q: host array
+ * of n_seq counts, each at most the sequence's length (0 skips the sequence),
+ * read before the call returns;
  * scores: host struct or NULL, read before the call returns.
  * workspace, ws_bytes: as for kvq_decode (the same buffer serves both; calls
  * that share it must not overlap on the GPU).

@@ -336,3 +336,28 @@ def test_keys_and_values_over_all_of_fp16(kb, vb, delta, d, G, most):
             m = [n if i == b else 0 for i, n in enumerate(n_q)]
             part = q[sum(n_q[:b]):sum(n_q[:b + 1])]
             _check(cache, spec, ks, vs, part, m, chunks=[lens[b]] if delta else None, **x)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("kb,vb,kw", [(2, 2, {}), (4, 2, dict(sink=4)), (4, 4, dict(akvq_delta=64)), (4, 2, dict(rotate=1))], ids=str)
+@pytest.mark.parametrize("size,most", [(400.0, 300.0), (20000.0, 30.0), (60000.0, 40000.0)])
+def test_large_queries_over_wide_keys(size, most, kb, vb, kw, dtype):
+    """Queries of some hundreds to 60000 against channels whose quantization steps are large: query times step is no fp16 number,
+    the score (with a scale that leaves it at a few units) is an ordinary one."""
+    hkv, gqa, d = 2, 4, 128
+    if kw.get("rotate"):
+        size, most = size / 32, most / 16       # (a rotated row must still be fp16 numbers)
+    lens, n_q = [200, 77, 130], [40, 1, 3]
+    spec = tl.kvq().CacheSpec(kb, vb, 32, d, hkv * gqa, hkv, 3, 256, **kw)
+    rng = np.random.default_rng(int(size) + kb)
+    ks, _ = _wide(rng, lens, hkv, d, most)
+    _, vs = _hist(rng, lens, hkv, d)
+    q = rng.uniform(-size, size, (sum(n_q), hkv * gqa, d)).astype(np.float32)
+    q[::3] /= 1000                              # and rows of ordinary size beside them
+    q = q.astype(np.float16).astype(np.float32) if dtype == "fp16" else tl.bf16_values(q) if dtype == "bf16" else q
+    cache = _filled(spec, ks, vs)
+    for x in (dict(scale=1.0 / (size * most)), dict(scale=4.0 / (size * most), cap=2.0)):
+        for b in range(3):
+            m = [n if i == b else 0 for i, n in enumerate(n_q)]
+            part = q[sum(n_q[:b]):sum(n_q[:b + 1])]
+            _check(cache, spec, ks, vs, part, m, dtype, chunks=[lens[b]] if kw.get("akvq_delta") else None, **x)

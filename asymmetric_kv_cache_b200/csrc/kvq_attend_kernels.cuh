@@ -384,6 +384,15 @@ __device__ __forceinline__ void att_fp16(AttState<D / 16>& st, const RowRule& rr
       mma16816(c[nt], q.x, q.y, q.z, q.w, row[0], row[4]);
     }
   }
+  // products with slots past `valid` out of the way before the scores: the
+  // warp chooses the tanh's form by all of its products
+  if (valid < 8 * NT) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (8 * nt + 2 * i4 + e >= valid) c[nt][e] = c[nt][e + 2] = 0.f;
+  }
   float s[NT][2];
   uint32_t pb[NT];
   att_scores<NT>(rr, c, 0.f, pos0, true, lane, s);

@@ -361,3 +361,21 @@ def test_large_queries_over_wide_keys(size, most, kb, vb, kw, dtype):
             m = [n if i == b else 0 for i, n in enumerate(n_q)]
             part = q[sum(n_q[:b]):sum(n_q[:b + 1])]
             _check(cache, spec, ks, vs, part, m, dtype, chunks=[lens[b]] if kw.get("akvq_delta") else None, **x)
+
+
+def test_results_do_not_follow_what_unused_slots_hold():
+    """The same tokens beside zeros, large numbers and NaN in the slots that no token has reached: the same bits."""
+    spec = tl.kvq().CacheSpec(4, 2, 32, 64, 4, 1, 1, 128, window=32, sink=20)
+    rng = np.random.default_rng(12)
+    for n in (1, 5, 30, 81):
+        ks, vs = _hist(rng, [n], 1, 64)
+        q = tl.to_device(_queries(rng, [min(n, 3)], 4, 64, "fp16"), "fp16")
+        outs = []
+        for held in (0.0, 30000.0, float("nan")):
+            cache = tl.kvq().KVQCache(spec)
+            cache.buffer[cache.layout["blocks_offset"]:].view(torch.float16).fill_(held)
+            torch.cuda.synchronize()
+            tl.append_chunks(cache, ks, vs, "fp16")
+            outs.append([cache.attend(q, [min(n, 3)], cap=cap).clone() for cap in (0.0, 50.0, 12.0)])
+        for other in outs[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(outs[0], other)), n

@@ -753,7 +753,8 @@ kvq_status kvq_workspace_status(const void* workspace, void* stream) {
   if (e != cudaSuccess) return cuda_fail(e, "reading the workspace error word");
   if (word != 0)
     return fail(KVQ_ERR_DEVICE,
-                "a decode kernel gave up a bounded wait or failed range check %d (word %#x)",
+                "a decode or attend kernel gave up a bounded wait, found the workspace's tickets not "
+                "zeroed, or failed range check %d (word %#x)",
                 word >> 8, (unsigned)word);
   return ok();
 }

@@ -708,8 +708,11 @@ __global__ void __launch_bounds__(kAttThreads, 4)
   if (tid == 0) {
     int* ticket = a.tickets + seqs.unit_off[sq] + unit;
     __threadfence();
-    last = atomic_add_acq_rel_gpu(ticket, 1) == parts - 1;
+    const int before = atomic_add_acq_rel_gpu(ticket, 1);
+    last = before == parts - 1;
     if (last) *ticket = 0;
+    // a workspace that something else has written: nobody would be the last
+    if ((uint32_t)before >= (uint32_t)parts) atomicExch(err, KVQ_ERR_DEVICE);
   }
   __syncthreads();
   if (!last) return;

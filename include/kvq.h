@@ -278,7 +278,10 @@ KVQ_API kvq_status kvq_append(kvq_cache* cache, const void* k, const void* v, kv
  * workspace: device buffer of at least the workspace_bytes reported by
  * kvq_cache_required_bytes, 256-byte aligned, zero-filled before its first
  * use (kvq_workspace_init).  Calls that share a workspace must not overlap
- * on the GPU.  For each chunk of up to 2048 sequences the call launches the
+ * on the GPU.  Where its parts lie depends on the configuration (max_seqs,
+ * heads, head_dim), and the tickets among them must be zero between calls: a
+ * cache of another configuration may use the same workspace only after it has
+ * been zero-filled again.  For each chunk of up to 2048 sequences the call launches the
  * split-K decode kernel (one CTA per SM) and, when units are split across
  * many CTAs, a small combine kernel that merges them (launched as a
  * programmatic dependent of the first).  Inside a CTA the warps claim key
@@ -357,8 +360,11 @@ typedef struct {
  * of n_seq counts, each at most the sequence's length (0 skips the sequence),
  * read before the call returns;
  * scores: host struct or NULL, read before the call returns.
- * workspace, ws_bytes: as for kvq_decode (the same buffer serves both; calls
- * that share it must not overlap on the GPU).
+ * workspace, ws_bytes: as for kvq_decode (the same buffer serves both calls of
+ * one cache, or of caches of one configuration; calls that share it must not
+ * overlap on the GPU).  A call that finds tickets which are not zero may leave
+ * rows of out unwritten, and records that (kvq_workspace_status); the workspace
+ * must then be zero-filled again.
  * The kernels read the lengths and prefix from the device, so a captured
  * call may be replayed as appends advance them; out is then of the newest
  * tokens at that time.  The cache's contents must be finite (as the append's
@@ -459,11 +465,13 @@ KVQ_API kvq_status kvq_decode_fp16(const void* k, const void* v, const int32_t* 
 /* Size in bytes of the fixed scratch array used by kvq_decode_noalloc. */
 KVQ_API size_t kvq_noalloc_scratch_bytes(void);
 
-/* Zero-fill a decode workspace on stream (cudaMemsetAsync). */
+/* Zero-fill a workspace of kvq_decode and kvq_attend on stream (cudaMemsetAsync). */
 KVQ_API kvq_status kvq_workspace_init(void* workspace, size_t ws_bytes, void* stream);
 
 /* Read the workspace error word (synchronous copy on stream): KVQ_OK, or
- * KVQ_ERR_DEVICE if some decode kernel gave up a bounded wait. */
+ * KVQ_ERR_DEVICE if some decode or attend kernel gave up a bounded wait or an
+ * attend found tickets that were not zero.  The word stays until the workspace
+ * is zero-filled. */
 KVQ_API kvq_status kvq_workspace_status(const void* workspace, void* stream);
 
 /* Refresh the host length mirror from the device copy (synchronizes

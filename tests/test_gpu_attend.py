@@ -379,3 +379,25 @@ def test_results_do_not_follow_what_unused_slots_hold():
             outs.append([cache.attend(q, [min(n, 3)], cap=cap).clone() for cap in (0.0, 50.0, 12.0)])
         for other in outs[1:]:
             assert all(torch.equal(a, b) for a, b in zip(outs[0], other)), n
+
+
+def test_a_workspace_that_was_not_zeroed_is_reported(monkeypatch):
+    """Tickets left over from something else: no block knows that it is the last one, so out is not written.  The call records
+    it, and zeroing the workspace mends it."""
+    monkeypatch.setenv("KVQ_ATTEND_TC", "0")
+    hkv, gqa, d, n = 1, 4, 128, 2000
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, 1, 2048)
+    rng = np.random.default_rng(13)
+    ks, vs = _hist(rng, [n], hkv, d)
+    cache = _filled(spec, ks, vs)
+    x = _queries(rng, [1], hkv * gqa, d, "fp16")
+    q = tl.to_device(x, "fp16")
+    torch.cuda.synchronize()
+    for held in (0.37, -2.5, 1e-40):
+        cache.workspace[256:].view(torch.float32).fill_(held)
+        cache.attend(q, [1])
+        torch.cuda.synchronize()
+        assert cache.workspace_status() == 10         # KVQ_ERR_DEVICE
+        assert tl.kvq().kvq_last_error()
+        cache.workspace.zero_()
+        _check(cache, spec, ks, vs, x, [1])

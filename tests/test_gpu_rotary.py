@@ -203,3 +203,44 @@ def test_captured_call_follows_the_lengths():
         graph.replay()
         torch.cuda.synchronize()
         _check(cache, qkv, hq, hkv, [n], [n * i], inv, got=out)
+
+
+def _guarded(cache, qkv, hq, hkv, n_new, lens, inv_freq, out_dtype, **kw):
+    """_check into outputs with two rows behind the last, which stay as they were."""
+    n, d = qkv.shape[0], cache.spec.head_dim
+    x = qkv.view(n, hq + 2 * hkv, d)
+    out = [torch.full((n + 2, h, d), 5.0, dtype=TYPES[out_dtype], device="cuda") for h in (hq, hkv, hkv)]
+    names = dict(qw="q_weight", kw="k_weight")
+    got = cache.norm_rotary(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], n_new, torch.from_numpy(inv_freq).cuda(),
+                            out_dtype=TYPES[out_dtype], out=[t[:n] for t in out], **{names.get(k, k): v for k, v in kw.items()})
+    _check(cache, qkv, hq, hkv, n_new, lens, inv_freq, out_dtype=out_dtype, got=got, **kw)
+    assert all((t[n:] == 5.0).all() for t in out)
+
+
+# kinds of call, each over rows on both sides of the rule that gives a block several rows (148 blocks of 8 rows of 16-bit types, of
+# 4 rows of fp32) and over last blocks of every fill
+KINDS = [dict(d=128, P=64), dict(d=64, P=32, interleaved=True), dict(d=64, P=31), dict(d=128, P=24, sections=[8, 10, 6]),
+         dict(d=128, P=37, sections=[12, 25], norm=False), dict(d=128, P=20, interleaved=True, sections=[3, 17])]
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+@pytest.mark.parametrize("dt,rows", [("fp16", 1183), ("bf16", 1184), ("fp16", 1185), ("bf16", 1191), ("fp16", 2006), ("fp32", 591),
+                                     ("fp32", 592), ("fp32", 593), ("fp32", 595), ("fp32", 1202)])
+def test_blocks_of_several_rows(dt, rows, kind):
+    d, P = kind["d"], kind["P"]
+    hq, hkv = (30, 5) if d == 64 else (12, 3)    # (40 and 18 heads: two passes of 32 and 16, the second not full)
+    g = torch.Generator("cuda").manual_seed(rows + P)
+    qkv = torch.randn((rows, (hq + 2 * hkv) * d), generator=g, device="cuda").to(TYPES[dt])
+    qw, kw = ((torch.rand(d, generator=g, device="cuda") + 0.5).to(TYPES[dt]) if kind.get("norm", True) else None for _ in range(2))
+    # short sequences, several to a block, and empty ones
+    rng = np.random.default_rng(rows)
+    n_new = []
+    while sum(n_new) < rows:
+        n_new.append(min(int(rng.choice([0, 1, 2, 3, 7, 60])), rows - sum(n_new)))
+    lens = [int(x) for x in rng.integers(0, 20000, len(n_new))]
+    pos = None
+    if "sections" in kind:
+        pos = torch.randint(0, 1 << 20, (len(kind["sections"]), rows), generator=g, device="cuda", dtype=torch.int32)
+    for out in ("fp16", "fp32"):
+        _guarded(_cache(d, hq, hkv, lens, None), qkv, hq, hkv, n_new, lens, _inv_freq(P), out, qw=qw, kw=kw, positions=pos,
+                 sections=kind.get("sections"), interleaved=kind.get("interleaved", False))

@@ -222,3 +222,38 @@ def test_python_refusals():
         with pytest.raises(K.KvqError):
             bad()
     assert cache.lengths() == [10, 20] == cache.device_lengths().tolist()
+
+
+@pytest.mark.parametrize("n,parent", [(333, [1, 1, 2]), (333, [1, 0, 0]), (500, [1, 1, 2]), (500, [1, 0, 0])])
+def test_shared_groups_of_adaptive_widths(n, parent):
+    """A prefix of 300 tokens by the same appends.  Sequences of one length hold its groups in the same bytes, which stay where
+    they are; sequences of different lengths hold some of them at different widths, and take over the other's."""
+    from tests.test_gpu_akvq import _append_schedule, _check_bytes, _hist as hist
+    G, shared = 32, 300
+    spec = tl.kvq().CacheSpec(4, 2, G, 64, 4, 2, 3, 1024, akvq_delta=64)
+    cfg, cache = tl.oracle_cfg(spec), tl.kvq().KVQCache(spec)
+    ks, vs = hist(np.random.default_rng(n), [333, n, 333], 2, 64)
+    for x in (ks, vs):
+        x[1][:shared] = x[2][:shared] = x[0][:shared]
+    chunks = _append_schedule(cache, ks, vs, [[shared, 33], [shared, n - shared], [shared, 20, 13]])
+    from oracle import kvq_oracle as o
+    bits = [o.akvq_cache_image(cfg, k, v, c)["bits"] for k, v, c in zip(ks, vs, chunks)]
+    assert (n == 333) == (bits[0][:shared // G] == bits[1][:shared // G]) and {2, 4} <= set(bits[1][:shared // G])
+    # a mark in group 1 of sequence 1: equal lengths leave the others' group alone, different ones take it over with the rest
+    mark = cache.block_bytes(1, 0, 2)[1]
+    was = mark[:16].clone()
+    mark[:16] ^= 255
+    cache.reorder(parent, shared=shared)
+    torch.cuda.synchronize()
+    if n == 333:
+        assert torch.equal(cache.block_bytes(0, 0, 2)[1][:16], was)
+        mark[:16] = was
+    else:
+        assert torch.equal(cache.block_bytes(0, 0, 2)[1][:16], was ^ 255)
+        for b in range(3):
+            if parent[b] == 1:
+                cache.block_bytes(b, 0, 2)[1][:16] = was
+    ks, vs, chunks = (oo.reorder(x, parent) for x in (ks, vs, chunks))
+    for b in range(3):
+        _check_bytes(cache, cfg, ks[b], vs[b], chunks[b], b)
+    assert cache.lengths() == [len(k) for k in ks] == cache.device_lengths().tolist()

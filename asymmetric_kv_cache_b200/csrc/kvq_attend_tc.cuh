@@ -561,7 +561,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool plain = a.cap == 0.f && !a.slopes;
       // this row of P: core matrices of 8 rows x 8 keys, a row eight 1024 bytes
       unsigned char* prow = smem + C::P_OFF + X * C::NP * C::P_BYTES + ((wrow & 127) + lane) / 8 * 1024 + lane % 8 * 16;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, base = 0.f;      // base: what the weights refer to, at m
+      bool far = false;                              // some row of the warp has an m of 2^20 or more
       const uint32_t ts = tm + lanes + C::T_S + kTcKeys * X, to = tm + lanes + C::T_O + D * X;
       for (int t = 0; t < nt; ++t) {
         att_tc_wait(&bars[C::B_S + X], t & 1, ok, err, lane);
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int c0 = 2 * (t0 + t);
         const bool every = c0 + 2 <= c_pre || (c0 >= c_lo && c0 + 2 <= c_hi);
         float mul = rr.scale2;
-        if (!(plain && every)) {
+        if (!(plain && every && !far)) {
           if (a.cap != 0.f) {
             att_cap(rr, s);
           } else {
@@ -613,9 +614,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float mx = max_of(s) * mul;
         if (__any_sync(0xffffffffu, mx > m + kTcSlack)) {
           const float mn = fmaxf(m, mx);
-          const float alpha = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
+          base = mn == -INFINITY ? 0.f : mn;
+          const float alpha = fast_exp2(m - base);
           m = mn;
           l *= alpha;
+          // far from 0 the multiply-add must not keep more of a product than the
+          // maximum did: at 2^32 the largest weight could have been 2^128
+          far = __any_sync(0xffffffffu, fabsf(m) >= 1048576.f && m != -INFINITY);
+          if (far && mul != 1.f) {
+#pragma unroll
+            for (int i = 0; i < kTcKeys; ++i) s[i] *= mul;
+            mul = 1.f;
+          }
           if (t > 0) {
             // O holds the tiles before this one
             att_tc_wait(&bars[C::B_PV + X], (t - 1) & 1, ok, err, lane);
@@ -633,7 +643,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             att_tc_fence_before();
           }
         }
-        const float base = m == -INFINITY ? 0.f : m;
         uint32_t p[kTcKeys / 2];
         const uint64_t mul_2 = pk2(mul, mul), base_2 = pk2(-base, -base);
         uint64_t sum[2] = {0ull, 0ull};

@@ -401,3 +401,25 @@ def test_a_workspace_that_was_not_zeroed_is_reported(monkeypatch):
         assert tl.kvq().kvq_last_error()
         cache.workspace.zero_()
         _check(cache, spec, ks, vs, x, [1])
+
+
+@pytest.mark.parametrize("size", [1e3, 1e6, 2e7, 4e9])
+@pytest.mark.parametrize("gqa,n_q", [(2, 1), (8, 1), (4, 40)])
+def test_scores_of_any_size(size, gqa, n_q):
+    """One key wins by far, by scores of some thousands to some billions, of either sign: its value is the result."""
+    hkv, d, n = 1, 128, 300
+    spec = tl.kvq().CacheSpec(4, 4, 32, d, hkv * gqa, hkv, 1, 320)
+    rng = np.random.default_rng(int(size) % 1000 + gqa)
+    ks = [np.full((n, hkv, d), -1.0, np.float16)]
+    vs = [np.tile(rng.integers(-8, 8, (n, hkv, 1)), (1, 1, d)).astype(np.float16)]
+    ks[0][200] = -0.5
+    q = np.full((n_q, gqa, d), 1.0, np.float32)
+    for sign in (1.0, -1.0):
+        # (the other sign: all keys but one at the top would tie; the row of the one is turned round)
+        k = [sign * ks[0] if sign > 0 else np.where(np.arange(n)[:, None, None] == 200, 1.0, 0.5) * np.ones((n, hkv, d))]
+        k = [x.astype(np.float16) for x in k]
+        cache = _filled(spec, k, vs)
+        out = cache.attend(tl.to_device(q, "fp16"), [n_q], scale=size / d)
+        torch.cuda.synchronize()
+        late = n - n_q + np.arange(n_q) >= 200
+        assert late.all() and (out.float().cpu().numpy() == float(vs[0][200, 0, 0])).all(), (sign, out.flatten()[:4])

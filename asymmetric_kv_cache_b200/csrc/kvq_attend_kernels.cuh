@@ -218,11 +218,22 @@ __device__ __forceinline__ void att_load_q(const void* q, int64_t at, int dtype,
   }
 }
 
+// The exponent that weights refer to at the maximum m: 2^lift times the largest
+// is still an fp16 number, and the small ones keep more bits before they are
+// subnormal (relative to 1, 3000 keys of 2^-20 to 2^-25 each beside one of 1
+// were 0.9 % off on register tiles, 7.9 % on the tensor cores).  Where fp32 no
+// longer holds m - lift well, m itself.
+template <int LIFT>
+__device__ __forceinline__ float att_base(float m) {
+  return fabsf(m) < 1048576.f ? m - (float)LIFT : m;
+}
+constexpr int kAttLift = 15;
+
 template <int MT>
 struct AttState {
   float o[MT][4];   // O^T: channels 16 mt + g8 (+ 8), rows 2 i4, 2 i4 + 1
   float m, l;       // row g8: running maximum (exp2 domain), sum over this lane's keys
-};
+};                  // (o and l relative to att_base(m))
 
 // Folds 8 NT keys' scores into the running softmax and returns the weights
 // as the B operand of the value product.
@@ -236,8 +247,8 @@ __device__ __forceinline__ void att_softmax(AttState<MT>& st, float (&s)[NT][2],
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
   const float mn = fmaxf(st.m, mx);
-  const float base = mn == -INFINITY ? 0.f : mn;   // no key seen yet: every weight is 0
-  const float alpha = fast_exp2(st.m - base);
+  const float base = mn == -INFINITY ? 0.f : att_base<kAttLift>(mn);   // no key seen yet: every weight is 0
+  const float alpha = fast_exp2(att_base<kAttLift>(st.m) - base);
   st.m = mn;
   if (__any_sync(0xffffffffu, alpha != 1.f)) {
     st.l *= alpha;
@@ -660,7 +671,7 @@ __global__ void __launch_bounds__(kAttThreads, 4)
       }
     }
     if (i4 == 0) {
-      mine[g8 * (D + 2) + D] = st.m;
+      mine[g8 * (D + 2) + D] = att_base<kAttLift>(st.m);
       mine[g8 * (D + 2) + D + 1] = st.l;
     }
   }

@@ -20,7 +20,8 @@
 //   * 4 warps per row tile, a thread per row, turn S into P, without exchange
 //     between threads.  The maximum that the weights refer to is only moved
 //     when a score passes it by 2^8, so O in tensor memory is rarely
-//     rescaled; weights stay below 2^8 and the sum is fp32.
+//     rescaled; weights are 2^7 at that maximum, stay below 2^15 and go to fp16
+//     (one rounding), and the sum, of the rounded ones, is fp32.
 // Rows of fp32 or rotated queries, which fp16 does not hold exactly, come as
 // value and residual in the two Q areas, one row tile per unit, and S gets
 // the third product Q2 K1^T.
@@ -42,6 +43,7 @@ constexpr int kTcRegs = 96, kTcRegsSoftmax = 136, kTcRegsOperands = 88, kTcRegsR
 static_assert(2 * kTcRegsSoftmax + 2 * kTcRegsOperands + kTcRegsRest <= 5 * kTcRegs,
               "the groups' registers come out of the launch's");
 constexpr float kTcSlack = 8.f;           // a maximum may be passed by 2^8 before O is rescaled
+constexpr int kTcLift = 7;                // the largest weight is then 2^15
 
 template <int D, int KB, int VB, int G>
 struct TcAtt {
@@ -614,8 +616,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float mx = max_of(s) * mul;
         if (__any_sync(0xffffffffu, mx > m + kTcSlack)) {
           const float mn = fmaxf(m, mx);
-          base = mn == -INFINITY ? 0.f : mn;
-          const float alpha = fast_exp2(m - base);
+          base = mn == -INFINITY ? 0.f : att_base<kTcLift>(mn);
+          const float alpha = fast_exp2(att_base<kTcLift>(m) - base);
           m = mn;
           l *= alpha;
           // far from 0 the multiply-add must not keep more of a product than the
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float* ps = reinterpret_cast<float*>(a.ws + w.partials_off) +
                     ((int64_t)blockIdx.x * seqs.slot_rows + wrow) * (D + 4);
         if (parts > 1 && lane < rows) {
-          ps[lane * (D + 4) + D] = m;
+          ps[lane * (D + 4) + D] = att_base<kTcLift>(m);
           ps[lane * (D + 4) + D + 1] = l;
         }
 #pragma unroll 4

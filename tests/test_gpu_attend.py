@@ -423,3 +423,25 @@ def test_scores_of_any_size(size, gqa, n_q):
         torch.cuda.synchronize()
         late = n - n_q + np.arange(n_q) >= 200
         assert late.all() and (out.float().cpu().numpy() == float(vs[0][200, 0, 0])).all(), (sign, out.flatten()[:4])
+
+
+@pytest.mark.parametrize("gqa,n_q", [(2, 1), (8, 1), (4, 40)])
+def test_many_small_weights(gqa, n_q):
+    """One key takes a weight of 1 and 2999 others between 2^-16 and 2^-25 each, and only those have a value.  A weight is fp16
+    relative to 2^15 times the largest (tensor cores: to at least 2^7 times): off by 2^-11 of itself or by 2^-25 2^-15 (2^-7).
+    The result is rounded (2^-11 of itself, 2^-25), and a score of up to 17.4 is off by 2^-17 times 3 times itself, twice in
+    the result."""
+    import os
+    hkv, d, n = 1, 128, 3000
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, 1, 3008)
+    ks, vs = [np.zeros((n, hkv, d), np.float16)], [np.full((n, hkv, d), 64.0, np.float16)]
+    ks[0][n // 3, :, 0], vs[0][n // 3] = 8.0, 0.0
+    cache = _filled(spec, ks, vs)
+    q = np.zeros((n_q, gqa, d), np.float32)
+    q[..., 0] = np.float16(np.linspace(11.0, 17.3, n_q * gqa).reshape(n_q, gqa) / 8.0)
+    out = cache.attend(tl.to_device(q, "fp16"), [n_q], scale=1.0)
+    want, _ = oo.attend(tl.oracle_cfg(spec), ks[0], vs[0], q, scale=1.0)
+    least = 2.0 ** (-25 - (7 if os.environ["KVQ_ATTEND_TC"] == "1" else 15))
+    off = np.abs(out.double().cpu().numpy() - want)
+    tol = want * (2 * 2.0 ** -11 + 2 * 3 * 17.4 * 2.0 ** -17) + n * least * 64 + 2.0 ** -25
+    assert (off <= tol).all(), ((off / tol).max(), (off / want).max())

@@ -230,13 +230,6 @@ __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, 
   lds_words<WV>(word(OFF_V + (kv * 32 + lane) * (4 * WV)), vw);
   lds_words<2 * J>(word(OFF_VS + (4 * kv + i4) * J * 8), vs);
   lds_words<2 * J>(word(OFF_VZ + (4 * kv + i4) * J * 8), vz);
-  // From the scales 4368 and 21840 on (bits below; scales are not negative) 15
-  // and 3 steps round to infinity in fp16.  A lane looks at its part of all.
-  constexpr uint32_t kWide = 0x8000u - (KBL == 4 ? 0x6C44u : 0x7555u);
-  uint32_t sw[D / 64], wide = 0;
-  lds_words<D / 64>(word(OFF_S) + lane * (D / 64), sw);
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) wide |= sw[i] + (kWide | kWide << 16);   // bit 15: at least that scale
   wait();
   // this lane's row of its matrix of four: neighbouring channel eights for the
   // keys, (channel eight, token eight) for the values
@@ -271,6 +264,15 @@ __device__ __forceinline__ void tc_fill_block(const unsigned char* blk, int hf, 
     });
     stmatrix4(v1 + 2 * mt * (kTcKeys / 8) * 128, o[0], o[1], o[2], o[3]);
   });
+  // From the scales 4368 and 21840 on (bits below; scales are not negative) 15
+  // and 3 steps round to infinity in fp16.  A lane looks at its part of all
+  // (read here again: read with the rest of the block, it made 2048 tokens of
+  // two 18k prompts, not capped, 1587 us instead of 1507).
+  constexpr uint32_t kWide = 0x8000u - (KBL == 4 ? 0x6C44u : 0x7555u);
+  uint32_t sw[D / 64], wide = 0;
+  lds_words<D / 64>(word(OFF_S) + lane * (D / 64), sw);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) wide |= sw[i] + (kWide | kWide << 16);   // bit 15: at least that scale
   // A channel whose keys spread over more than 65504: s code was infinite above
   // though s code + z is not.  The block's keys are written again from fp32,
   // whose products are exact and whose sums are off by 2^-24 (a short loop over

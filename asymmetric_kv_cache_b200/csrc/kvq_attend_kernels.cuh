@@ -15,8 +15,9 @@
 //
 // One block (32 or 64 tokens, taken 32 at a time) is, per warp:
 //   * k = s_c code + z_c, so q.k = sum_c (q_c s_c) code_c + sum_c q_c z_c.
-//     The codes go to the tensor core as exact small integers; q_c s_c is an
-//     fp16 value plus its exact residual (one fused multiply-subtract), rows
+//     The codes go to the tensor core as exact small integers; q_c s_c (of a
+//     query that is divided by a power of two where the product could leave
+//     fp16) is an fp16 value plus its exact residual (one fused multiply-subtract), rows
 //     0-7 of the 16-row A operand holding the one and rows 8-15 the other,
 //     so the logits carry ~22 bits at no extra tile.
 //   * p goes to fp16 (one rounding, relative 2^-11 at most, and the sum is of
@@ -164,8 +165,8 @@ __device__ __forceinline__ void att_cap_poly(const RowRule& rr, const float (&co
 // coefficients for T = 1/2 (off by 2.6e-7 in fp32: 1.3e-5 in a score capped at
 // 50, a twentieth of the weight's rounding to fp16), seven for T = 1 (1.0e-7).
 // Elsewhere 1 - 2 / (1 + e^(2t)), off by a few 2^-24, which takes two special
-// function results a score, of which an SM gives 16 a cycle: the 7268 us of
-// that form alone for 2048 tokens over two contexts of 18k became 2829.
+// function results a score, of which an SM gives 16 a cycle: with that form
+// alone 2048 tokens over two contexts of 18k take 2672 us, not 2230.
 template <int N>
 __device__ __forceinline__ void att_cap(const RowRule& rr, float (&x)[N]) {
   constexpr float kP4[4] = {0.999999464f, -0.333262831f, 0.131899402f, -0.0443927385f};

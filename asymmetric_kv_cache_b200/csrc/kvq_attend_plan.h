@@ -30,9 +30,13 @@ inline int attend_tc_rows(const Geom& g, const int32_t* lens, const int32_t* n_q
 //
 // A unit is (sequence, kv head, tile of unit_rows rows).  With at least as
 // many units as resident CTAs every unit is one piece.  Otherwise the units
-// are cut into about max_ctas pieces, a sequence's units in proportion to
-// the keys that they see, into no pieces of fewer than four steps, and into
-// no more than the partials have room for.  The lengths are the host's; the
+// are cut into at most `want` pieces, a sequence's units in proportion to the
+// keys that they see (rounded down) and into no pieces of fewer than four
+// steps.  `want` is max_ctas or, where that is less, the partials' room less
+// one slot for each unit that ends up whole: 148 - units for the tensor cores'
+// 256 rows a slot, so that from 50 equal units on every unit is one piece (one
+// sequence of 32768 with 384 new tokens: 48 units in 96 pieces; with 400 to
+// 1100: 56 to 144 whole units).  The lengths are the host's; the
 // kernels cut what they find in the device's into the same number of pieces,
 // so a replayed launch stays right when they have grown.  Returns whether
 // some unit is cut.

@@ -24,10 +24,11 @@ constexpr int kAttendMergeParts = 32;
 // kAttendRows) goes to the tensor-core kernel, if the call's such sequences
 // give the other one at least so many steps (8 rows against 32 keys of 128
 // channels; it does about 780 a us).  Measured, register tiles / tensor cores,
-// us, 32 query and 8 kv heads of 128: 8 x 4113 keys: 24 rows 41 / 50, 32 rows
-// 55 / 52, 48 rows 93 / 53; one context of 32768: 43 / 51, 53 / 51, 71 / 50;
-// 64 x 2048: 132 / 192, 166 / 193, 244 / 193; 16 x 1000: 29 / 28, 29 / 28, 43 /
-// 28; with 4 kv heads of 64 (6 thousand steps at 48 rows) 18 / 26.
+// us, 32 query and 8 kv heads of 128: 8 x 4113 keys: 24 rows 41 / 51, 32 rows
+// 55 / 52, 36 rows 94 / 53 (capped 43 / 65, 58 / 67, 99 / 67); one context of
+// 32768: 44 / 52, 53 / 52, 65 / 52; 64 x 2048: 133 / 204, 167 / 206, 212 / 206;
+// 16 x 1000: 29 / 29, 29 / 28, 38 / 29; with 4 kv heads of 64 (6 thousand steps
+// at 48 rows) 19 / 22.
 constexpr int kAttendTcRows = 33;
 constexpr int kAttendTcSteps = 16384;
 

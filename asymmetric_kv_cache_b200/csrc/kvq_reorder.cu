@@ -3,11 +3,13 @@
 //
 // The host turns the map b <- parent[b] into chains of batches of at most
 // kReorderBatch moves (kvq_reorder_plan.h).  A batch is "read every source,
-// then write every destination", and no batch reads what an earlier batch of
-// its chain wrote.  Every 16-byte unit of the layout has one owner thread per
+// then write every destination".  A later batch of a chain may read what an
+// earlier one wrote (a cycle of more than kReorderBatch sequences goes on from
+// a member that its batch before has written), so the batches of a chain must
+// stay in order.  Every 16-byte unit of the layout has one owner thread per
 // chain, and the unit's bytes in one sequence only ever go to the same unit
-// of another, so a thread that walks the chain's batches in order keeps the
-// map exact with no scratch copy and no barrier between blocks.
+// of another: a thread that walks the chain's batches in order keeps the map
+// exact with no scratch copy and no barrier between blocks.
 //
 // Bound: memory; every moved byte is read once and written once.  Blocks
 // whose tokens the caller declares shared are not touched.  A thread reads
@@ -76,7 +78,8 @@ __device__ __forceinline__ void move_units(const Geom& g, unsigned char* at, int
 // Grid: x = tiles of kReorderTile units over (kv head, area), strided; y =
 // chain.  NB: the largest batch of the launch, rounded up to a power of two.  A
 // thread has 8 loads of 16 bytes in flight whatever NB is, 1024 threads on an
-// SM: 128 KB, three times what the memory's latency at its rate needs.
+// SM (768 with NB = 8): 128 KB (96), three times (twice) what the memory's
+// latency at its rate needs.
 template <int NB, bool AK>
 __global__ void __launch_bounds__(kReorderThreads, NB == 8 ? 3 : 4)
     reorder_kernel(const Geom g, unsigned char* cache, const ReorderMoves mv, int32_t shared_tokens) {

@@ -11,7 +11,7 @@
 // it becomes fp32: in fp32 the product of a position of 10^5 and a frequency
 // near 1 is already off by 2^-8 rad.  A block computes the P angles of its
 // row once (P fp64 products and as many sincospi) and every head of the row
-// uses them from registers.
+// reads them from shared memory.
 //
 // A head row is D / 8 lanes.  A lane owns two pieces of 4 channels: the same
 // four of a pair's two halves (or 8 neighbours, where pairs are neighbours, or
@@ -107,7 +107,8 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 // bf16 to fp16 (393 MB), us: one row to a block, from memory into registers,
 // 158; four rows, the partner by shuffles, 119; pairs in a lane 113; 8 rows, a
 // head through all of them, the next two rows' loads under way, 103; with the
-// copies 72 (65 without the norms): 5.4 TB/s, 0.83 of the measured copy.  The
+// copies 72 (65 without the norms): 5.4 TB/s, 0.83 of the measured copy, back
+// to back (75 to 79 among other calls through the Python entry point).  The
 // time between load and use had bound it, not issue: packed fp32 arithmetic
 // left it at 74, five blocks on an SM (48 registers) made it 90, two rows
 // unrolled 74.

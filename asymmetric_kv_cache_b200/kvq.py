@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from array import array
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -49,6 +50,15 @@ class KvqLayout(ctypes.Structure):
         "vcodes_offset", "vscale_offset", "vmin_offset", "tail_slots", "sinks_offset",
         "sink_bytes", "sink_slots", "akvq_block_bytes", "akvq_kscale_offset", "akvq_kmin_offset",
         "akvq_vcodes_offset", "akvq_vscale_offset", "akvq_vmin_offset")]
+
+
+_NOWHERE = nullcontext()
+
+
+def _on(stream):
+    """Where a call allocates its outputs: on the stream that writes them.  The current stream's allocator may hand out memory
+    that kernels of the current stream still read, and would take it back before another stream's have written it."""
+    return _NOWHERE if stream is None else torch.cuda.stream(stream)
 
 
 def _int32s(values, name: str):
@@ -314,7 +324,8 @@ class KVQCache:
         """Attention of the newest ``n_q[b]`` tokens of each sequence (kvq_attend).
 
         q: [sum(n_q), n_q_heads, d]; scale (0: 1 / sqrt(d)), cap, window: numbers, 0 for none;
-        slopes: fp32 [n_q_heads], prefix: int32 [n_seq], on the device.  Returns fp16 like q.
+        slopes: fp32 [n_q_heads], prefix: int32 [n_seq], on the device.  Returns fp16 like q, written to
+        ``out`` if given, else to a new tensor of ``stream``.
         """
         dt = DTYPE_CODES.get(q.dtype)
         if dt is None:
@@ -329,7 +340,8 @@ class KVQCache:
                        None if slopes is None else self._ptr(slopes, "slopes", torch.float32, (sp.n_q_heads,)),
                        None if prefix is None else self._ptr(prefix, "prefix", torch.int32, (n_seq,)))
         if out is None:
-            out = torch.empty(shape, dtype=torch.float16, device=q.device)
+            with _on(stream):
+                out = torch.empty(shape, dtype=torch.float16, device=q.device)
         self._launch("kvq_attend", kvq_attend, stream, self._h, qp, dt, arr.buffer_info()[0], n_seq, ctypes.byref(sc),
                      self._ptr(out, "out", torch.float16, shape), self.workspace.data_ptr(),
                      self.workspace.numel())
@@ -358,7 +370,8 @@ class KVQCache:
         one projection output); inv_freq: fp32 [pairs]; q_weight, k_weight: [d] of the rows' type,
         None for no norm; positions: None (the cache's lengths + 0, 1, ..) or int32 [rows] or
         [axes, rows] with the pairs of each axis in ``sections``.  Returns contiguous (q, k, v) of
-        ``out_dtype`` (v None if it was), written to ``out`` if three tensors are given.
+        ``out_dtype`` (v None if it was), written to ``out`` if three tensors are given, else to new
+        tensors of ``stream``.
         """
         dt, odt = DTYPE_CODES.get(q.dtype), DTYPE_CODES.get(out_dtype)
         if dt is None or odt is None:
@@ -390,8 +403,9 @@ class KVQCache:
             raise ValueError("sections go with positions")
         if out is None:
             dev = q.device
-            out = (torch.empty(q_shape, dtype=out_dtype, device=dev), torch.empty(k_shape, dtype=out_dtype, device=dev),
-                   None if v is None else torch.empty(k_shape, dtype=out_dtype, device=dev))
+            with _on(stream):
+                out = (torch.empty(q_shape, dtype=out_dtype, device=dev), torch.empty(k_shape, dtype=out_dtype, device=dev),
+                       None if v is None else torch.empty(k_shape, dtype=out_dtype, device=dev))
         qo, ko, vo = out
         if qo is None or ko is None or (vo is None) != (v is None):
             raise ValueError("out must hold a tensor for each of q, k and v")

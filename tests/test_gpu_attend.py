@@ -445,3 +445,27 @@ def test_many_small_weights(gqa, n_q):
     off = np.abs(out.double().cpu().numpy() - want)
     tol = want * (2 * 2.0 ** -11 + 2 * 3 * 17.4 * 2.0 ** -17) + n * least * 64 + 2.0 ** -25
     assert (off <= tol).all(), ((off / tol).max(), (off / want).max())
+
+
+def test_outputs_on_another_stream():
+    """A call on a stream of its own, while the current one still reads memory that a tensor has given back: the new output is not
+    put there."""
+    hkv, gqa, d, n = 1, 4, 128, 40
+    spec = tl.kvq().CacheSpec(4, 2, 32, d, hkv * gqa, hkv, 1, 64)
+    rng = np.random.default_rng(14)
+    ks, vs = _hist(rng, [n], hkv, d)
+    cache = _filled(spec, ks, vs)
+    x = _queries(rng, [n], hkv * gqa, d, "fp16")
+    q = tl.to_device(x, "fp16")
+    kept = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        held = torch.full_like(q, 3.0)
+        torch.cuda._sleep(50_000_000)           # (some 30 ms of the current stream)
+        kept.copy_(held)
+        del held
+        out = cache.attend(q, [n], stream=side)
+        torch.cuda.synchronize()
+        assert (kept == 3.0).all()
+        _check(cache, spec, ks, vs, x, [n], out=out)

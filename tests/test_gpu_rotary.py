@@ -244,3 +244,24 @@ def test_blocks_of_several_rows(dt, rows, kind):
     for out in ("fp16", "fp32"):
         _guarded(_cache(d, hq, hkv, lens, None), qkv, hq, hkv, n_new, lens, _inv_freq(P), out, qw=qw, kw=kw, positions=pos,
                  sections=kind.get("sections"), interleaved=kind.get("interleaved", False))
+
+
+def test_outputs_on_another_stream():
+    """A call on a stream of its own, while the current one still reads memory that tensors have given back: the new outputs are
+    not put there."""
+    d, hq, hkv, n = 64, 4, 4, 30
+    cache = _cache(d, hq, hkv, [9])
+    qkv = torch.randn((n, 12 * d), device="cuda").half()
+    x, f = qkv.view(n, 12, d), torch.from_numpy(_inv_freq(32)).cuda()
+    kept, side = torch.empty((12, n, hq, d), dtype=torch.float16, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        held = [torch.full_like(kept[0], 3.0) for _ in range(12)]
+        torch.cuda._sleep(50_000_000)           # (some 30 ms of the current stream)
+        for i in range(12):
+            kept[i].copy_(held[i])
+        del held
+        got = cache.norm_rotary(x[:, :hq], x[:, hq:2 * hq], x[:, 2 * hq:], [n], f, stream=side)
+        torch.cuda.synchronize()
+        assert (kept == 3.0).all()
+        _check(cache, qkv, hq, hkv, [n], [9], _inv_freq(32), got=got)
